@@ -21,7 +21,10 @@ __all__ = ["Graph", "layer_desc", "egnn_build_graph", "egnn_build_graph_noalloc"
            "egnn_hblocks", "egnn_hblocks_label_rows", "egnn_timing_enable", "egnn_timing_collect",
            "egnn_timing_reset", "GraphBuilder", "LayerBuffers", "EgnnError", "EGNN_F32", "EGNN_BF16",
            "Basis", "Orbitals", "egnn_label_width", "egnn_orbital_layout", "egnn_matrix_to_label",
-           "egnn_label_to_matrix", "egnn_edge_update_fwd", "egnn_edge_update_bwd", "egnn_assemble_bsr"]
+           "egnn_label_to_matrix", "egnn_edge_update_fwd", "egnn_edge_update_bwd", "egnn_assemble_bsr",
+           "attn_desc", "AttnBuffers", "egnn_diff_attention_sizes", "egnn_diff_attention_fwd",
+           "egnn_diff_attention_bwd", "egnn_distance_borders", "egnn_distance_bias_fwd", "egnn_distance_bias_bwd",
+           "dropout_desc", "egnn_dropout_fwd", "egnn_dropout_bwd"]
 
 _STORAGE = {EGNN_F32: torch.float32, EGNN_BF16: torch.bfloat16}
 
@@ -420,6 +423,278 @@ def egnn_edge_update_bwd(desc, graph: Graph, geom, weights, x, buffers, grad_e_o
         ct.byref(desc), ct.byref(g), _ptr(geom), _ptr(weights), _ptr(x), _ptr(buffers.saved), _ptr(grad_e_out),
         _ptr(grad_x), _ptr(grad_w), _ptr(buffers.ws), buffers.ws.numel(), _stream()))
     return grad_x, grad_w
+
+
+def _on_one_device(named):
+    """The GPU that every given tensor lives on (None entries are skipped)."""
+    dev = None
+    for name, t in named:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must live on the GPU")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+    return dev
+
+
+def _data(t):
+    return None if t is None else ct.c_void_p(t.data_ptr())
+
+
+def _expect_rng(rng, p):
+    if rng is not None:
+        _expect(rng, "rng", torch.int64, (2,))
+    elif not float(p) * 65536 < 0.5:
+        raise ValueError("rng ({seed, step}, int64 on the GPU) is required when the dropout probability is not zero")
+
+
+def attn_desc(lmax, C, n_heads, head_dim, scale=None, drop_p=0.0, site=0, storage=EGNN_F32):
+    """Differential attention over value rows [(lmax+1)^2][C]; scale defaults to 1/sqrt(head_dim)."""
+    if scale is None:
+        scale = float(head_dim) ** -0.5 if head_dim > 0 else 1.0
+    return _lib.EgnnAttnDesc(lmax, C, n_heads, head_dim, storage, site, 0, 0, 0, float(scale), float(drop_p))
+
+
+def egnn_diff_attention_sizes(desc, graph: Graph):
+    """(saved, inference workspace, training workspace) bytes."""
+    s, i, t = ct.c_size_t(), ct.c_size_t(), ct.c_size_t()
+    g = graph.c_struct()
+    _lib.check("egnn_diff_attention_sizes", _lib.load().egnn_diff_attention_sizes(
+        ct.byref(desc), ct.byref(g), ct.byref(s), ct.byref(i), ct.byref(t)))
+    return s.value, i.value, t.value
+
+
+class AttnBuffers:
+    """What the attention's backward reads and the workspaces, for one graph (allocated by torch)."""
+
+    def __init__(self, desc, graph: Graph, train=True):
+        saved, infer, tr = egnn_diff_attention_sizes(desc, graph)
+        dev = graph.row_ptr.device
+        self.saved = torch.empty(max(saved, 1), dtype=torch.uint8, device=dev) if train else None
+        self.ws = torch.empty(max(tr if train else infer, 1), dtype=torch.uint8, device=dev)
+
+
+def _expect_rows(t, name, dtype, shape, rows):
+    """Rows whose elements are packed, any distance apart; returns that distance in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape[1:]) != shape or t.dim() != len(shape) + 1:
+        raise ValueError(f"{name} must have shape (rows, {', '.join(map(str, shape))}), got {tuple(t.shape)}")
+    if t.shape[0] < rows:
+        raise ValueError(f"{name} needs at least {rows} rows, got {t.shape[0]}")
+    width = 1
+    for size, stride in zip(reversed(shape), reversed(t.stride()[1:])):
+        if size > 1 and stride != width:
+            raise ValueError(f"the elements of a row of {name} must be packed, strides are {t.stride()}")
+        width *= size
+    if rows <= 1:
+        return 0
+    if t.stride(0) < width:
+        raise ValueError(f"the rows of {name} overlap: stride {t.stride(0)}, width {width}")
+    return t.stride(0)
+
+
+def _expect_graph(graph: Graph, grouped=False):
+    _expect(graph.row_ptr, "graph.row_ptr", torch.int32, (graph.n_dst + 1,))
+    _expect(graph.src, "graph.src", torch.int32, (None,), min_rows=graph.n_edges)
+    if grouped:
+        if graph.src_ptr is None or graph.src_perm is None:
+            raise ValueError("the backward needs the graph grouped by source (egnn_group_sources)")
+        _expect(graph.src_ptr, "graph.src_ptr", torch.int32, (graph.n_src + 1,))
+        _expect(graph.src_perm, "graph.src_perm", torch.int32, (None,), min_rows=graph.n_edges)
+
+
+def _check_attn(desc, graph: Graph, q, k, v, lam, rng, grouped=False):
+    """Checks what both directions read; returns the description with the tensors' strides and (K, storage dtype)."""
+    if desc.storage not in _STORAGE:
+        raise ValueError(f"unknown storage type {desc.storage}")
+    dt, H, D, C, K = _STORAGE[desc.storage], desc.n_heads, desc.head_dim, desc.C, (desc.lmax + 1) ** 2
+    _expect_graph(graph, grouped)
+    d = _lib.EgnnAttnDesc.from_buffer_copy(desc)
+    d.q_stride = _expect_rows(q, "q", dt, (H, 2, D), graph.n_dst)
+    d.k_stride = _expect_rows(k, "k", dt, (H, 2, D), graph.n_src)
+    d.v_stride = _expect_rows(v, "v", dt, (K, C), graph.n_src)
+    _expect(lam, "lam", torch.float32, (H,))
+    _expect_rng(rng, desc.drop_p)
+    return d, K, dt
+
+
+def egnn_diff_attention_fwd(desc, graph: Graph, q, k, v, lam, bias=None, mask=None, rng=None, out=None, buffers=None):
+    """Differential attention of every row over its incoming edges: (out [n_dst][K][C], buffers).
+
+    q [n_dst][H][2][D], k [n_src][H][2][D], v [n_src][K][C] in the storage
+    type (rows may be slices of a wider array), lam [H]; bias [E][2H] or
+    [E][H][2]; mask [E] uint8 or bool, 0 = the edge takes no part; rng int64
+    [2] = {seed, step} on the GPU, needed for dropout.  buffers made with
+    train=True keep what the backward reads; without buffers the call makes
+    its own for inference.
+    """
+    lib = _lib.load()
+    d, K, dt = _check_attn(desc, graph, q, k, v, lam, rng)
+    E, H = graph.n_edges, desc.n_heads
+    if bias is not None:
+        _expect(bias.reshape(-1) if isinstance(bias, torch.Tensor) and bias.is_contiguous() else bias, "bias",
+                torch.float32, (E * 2 * H,))
+    if mask is not None:
+        if isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
+            mask = mask.view(torch.uint8)
+        _expect(mask, "mask", torch.uint8, (E,))
+    dev = _on_one_device([("graph.row_ptr", graph.row_ptr), ("graph.src", graph.src), ("q", q), ("k", k), ("v", v),
+                          ("lam", lam), ("bias", bias), ("mask", mask), ("rng", rng), ("out", out)]
+                         + ([("buffers.saved", buffers.saved), ("buffers.ws", buffers.ws)] if buffers else []))
+    with torch.cuda.device(dev):
+        if buffers is None:
+            buffers = AttnBuffers(desc, graph, train=False)
+        saved, infer, train = egnn_diff_attention_sizes(d, graph)
+        if buffers.saved is not None:
+            _expect_bytes(buffers.saved, "buffers.saved", saved)
+        _expect_bytes(buffers.ws, "buffers.ws", infer if buffers.saved is None else train)
+        if out is None:
+            out = torch.empty((graph.n_dst, K, desc.C), dtype=dt, device=dev)
+        _expect(out, "out", dt, (graph.n_dst, K, desc.C))
+        g = graph.c_struct()
+        _lib.check("egnn_diff_attention_fwd", lib.egnn_diff_attention_fwd(
+            ct.byref(d), ct.byref(g), _data(q), _data(k), _data(v), _data(lam), _data(bias), _data(mask), _data(rng),
+            _data(out), _data(buffers.saved), _data(buffers.ws), buffers.ws.numel(), _stream()))
+    return out, buffers
+
+
+def egnn_diff_attention_bwd(desc, graph: Graph, q, k, v, lam, buffers, grad_out, rng=None):
+    """(grad_q, grad_k, grad_v, grad_lam, grad_bias [E][2H]) of <grad_out, out>, fp32.
+
+    buffers are those of the forward on the same inputs (train=True); the
+    graph needs its source grouping; grad_bias is the gradient of the logits.
+    """
+    lib = _lib.load()
+    d, K, _ = _check_attn(desc, graph, q, k, v, lam, rng, grouped=True)
+    E, H, D, C = graph.n_edges, desc.n_heads, desc.head_dim, desc.C
+    _expect(grad_out, "grad_out", torch.float32, (graph.n_dst, K, C))
+    if buffers is None or buffers.saved is None:
+        raise ValueError("the backward needs buffers made with train=True")
+    dev = _on_one_device([("graph.row_ptr", graph.row_ptr), ("graph.src", graph.src), ("graph.src_ptr", graph.src_ptr),
+                          ("graph.src_perm", graph.src_perm), ("q", q), ("k", k), ("v", v), ("lam", lam),
+                          ("rng", rng), ("grad_out", grad_out), ("buffers.saved", buffers.saved),
+                          ("buffers.ws", buffers.ws)])
+    with torch.cuda.device(dev):
+        saved, _, train = egnn_diff_attention_sizes(d, graph)
+        _expect_bytes(buffers.saved, "buffers.saved", saved)
+        _expect_bytes(buffers.ws, "buffers.ws", train)
+        f32 = dict(dtype=torch.float32, device=dev)
+        gq = torch.empty((graph.n_dst, H, 2, D), **f32)
+        gk = torch.empty((graph.n_src, H, 2, D), **f32)
+        gv = torch.empty((graph.n_src, K, C), **f32)
+        gl = torch.empty(H, **f32)
+        gb = torch.empty((E, 2 * H), **f32)
+        g = graph.c_struct()
+        _lib.check("egnn_diff_attention_bwd", lib.egnn_diff_attention_bwd(
+            ct.byref(d), ct.byref(g), _data(q), _data(k), _data(v), _data(lam), _data(rng), _data(buffers.saved),
+            _data(grad_out), _data(gq), _data(gk), _data(gv), _data(gl), _data(gb), _data(buffers.ws),
+            buffers.ws.numel(), _stream()))
+    return gq, gk, gv, gl, gb
+
+
+def egnn_distance_borders(n_buckets, n_linear, r_linear, r_max):
+    """Bucket borders (CPU float32 [n_buckets - 1]): n_linear of equal width up to r_linear, then equal ratios."""
+    out = torch.empty(max(int(n_buckets) - 1, 0), dtype=torch.float32)
+    _lib.check("egnn_distance_borders", _lib.load().egnn_distance_borders(
+        int(n_buckets), int(n_linear), float(r_linear), float(r_max),
+        ct.cast(out.data_ptr(), ct.POINTER(ct.c_float))))
+    return out
+
+
+def _check_bias(graph: Graph, borders, n_buckets, n_columns):
+    _expect(borders, "borders", torch.float32, (n_buckets - 1,))
+    _expect(graph.dist, "graph.dist", torch.float32, (None,), min_rows=graph.n_edges)
+    return _lib.EgnnBiasDesc(n_buckets, n_columns)
+
+
+def egnn_distance_bias_fwd(graph: Graph, borders, table, out=None):
+    """bias [E][n_columns] = table[bucket of each edge's length]; borders [n_buckets - 1] ascending."""
+    _expect(table, "table", torch.float32, (None, None))
+    B, M = table.shape
+    d = _check_bias(graph, borders, B, M)
+    if out is not None:
+        _expect(out, "out", torch.float32, (graph.n_edges, M))
+    dev = _on_one_device([("graph.dist", graph.dist), ("borders", borders), ("table", table), ("out", out)])
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((graph.n_edges, M), dtype=torch.float32, device=dev)
+        g = graph.c_struct()
+        _lib.check("egnn_distance_bias_fwd", _lib.load().egnn_distance_bias_fwd(
+            ct.byref(d), ct.byref(g), _data(borders), _data(table), _data(out), _stream()))
+    return out
+
+
+def egnn_distance_bias_bwd(graph: Graph, borders, grad_bias):
+    """grad_table [n_buckets][n_columns]: grad_bias [E][n_columns] summed over each bucket's edges."""
+    lib = _lib.load()
+    _expect(grad_bias, "grad_bias", torch.float32, (graph.n_edges, None))
+    if not isinstance(borders, torch.Tensor):
+        raise ValueError("borders must be a torch tensor")
+    B, M = borders.numel() + 1, grad_bias.shape[1]
+    d = _check_bias(graph, borders, B, M)
+    dev = _on_one_device([("graph.dist", graph.dist), ("borders", borders), ("grad_bias", grad_bias)])
+    with torch.cuda.device(dev):
+        g = graph.c_struct()
+        nbytes = ct.c_size_t()
+        _lib.check("egnn_distance_bias_workspace",
+                   lib.egnn_distance_bias_workspace(ct.byref(d), ct.byref(g), ct.byref(nbytes)))
+        ws = torch.empty(max(nbytes.value, 1), dtype=torch.uint8, device=dev)
+        out = torch.empty((B, M), dtype=torch.float32, device=dev)
+        _lib.check("egnn_distance_bias_bwd", lib.egnn_distance_bias_bwd(
+            ct.byref(d), ct.byref(g), _data(borders), _data(grad_bias), _data(out), _data(ws), nbytes.value,
+            _stream()))
+    return out
+
+
+_SHARE = {"channel": _lib.EGNN_DROP_CHANNEL, "degree": _lib.EGNN_DROP_DEGREE, "row": _lib.EGNN_DROP_ROW}
+
+
+def dropout_desc(lmax, C, p, share="channel", site=0, storage=EGNN_F32):
+    """Dropout of rows [(lmax+1)^2][C]; share: one decision per "channel", per "degree" and channel, or per "row"."""
+    if share not in _SHARE:
+        raise ValueError(f"unknown sharing {share!r}, one of {sorted(_SHARE)}")
+    return _lib.EgnnDropoutDesc(lmax, C, _SHARE[share], storage, site, float(p))
+
+
+def egnn_dropout_fwd(desc, x, rng, residual=None, out=None):
+    """residual + keep/(1-p) x for x [rows][K][C]; rng int64 [2] = {seed, step} on the GPU (None when p is 0)."""
+    if desc.storage not in _STORAGE:
+        raise ValueError(f"unknown storage type {desc.storage}")
+    dt, shape = _STORAGE[desc.storage], (None, (desc.lmax + 1) ** 2, desc.C)
+    _expect(x, "x", dt, shape)
+    if residual is not None:
+        _expect(residual, "residual", dt, tuple(x.shape))
+    if out is not None:
+        _expect(out, "out", dt, tuple(x.shape))
+    _expect_rng(rng, desc.p)
+    dev = _on_one_device([("x", x), ("residual", residual), ("rng", rng), ("out", out)])
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty_like(x)
+        _lib.check("egnn_dropout_fwd", _lib.load().egnn_dropout_fwd(
+            ct.byref(desc), x.shape[0], _data(x), _data(residual), _data(rng), _data(out), _stream()))
+    return out
+
+
+def egnn_dropout_bwd(desc, grad_y, rng, out=None):
+    """Gradient with respect to x for the forward's decisions (that of residual is grad_y itself), fp32."""
+    _expect(grad_y, "grad_y", torch.float32, (None, (desc.lmax + 1) ** 2, desc.C))
+    if out is not None:
+        _expect(out, "out", torch.float32, tuple(grad_y.shape))
+    _expect_rng(rng, desc.p)
+    dev = _on_one_device([("grad_y", grad_y), ("rng", rng), ("out", out)])
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty_like(grad_y)
+        _lib.check("egnn_dropout_bwd", _lib.load().egnn_dropout_bwd(
+            ct.byref(desc), grad_y.shape[0], _data(grad_y), _data(rng), _data(out), _stream()))
+    return out
 
 
 def _hdesc(lmax, C, shell_l, storage):

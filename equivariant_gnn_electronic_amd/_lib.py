@@ -10,6 +10,7 @@ LIB_PATH = os.environ.get("EGNN_LIBRARY") or os.path.join(os.path.dirname(os.pat
 
 EGNN_OK, EGNN_E_ARG, EGNN_E_CAPACITY, EGNN_E_HIP, EGNN_E_UNSUPPORTED, EGNN_E_WORKSPACE = range(6)
 EGNN_F32, EGNN_BF16 = 0, 1
+EGNN_DROP_CHANNEL, EGNN_DROP_DEGREE, EGNN_DROP_ROW = 0, 1, 2
 
 # every symbol the header declares, with (restype, argtypes)
 _vp, _i32, _i64, _u32, _f64, _sz = ct.c_void_p, ct.c_int32, ct.c_int64, ct.c_uint32, ct.c_double, ct.c_size_t
@@ -41,6 +42,21 @@ class EgnnOrbitals(ct.Structure):
                 ("atom_orb", _vp), ("atom_mol", _vp), ("mol_norb", _vp), ("mat_off", _vp)]
 
 
+class EgnnAttnDesc(ct.Structure):
+    _fields_ = [("lmax", ct.c_int32), ("C", ct.c_int32), ("n_heads", ct.c_int32), ("head_dim", ct.c_int32),
+                ("storage", ct.c_int32), ("site", ct.c_uint32), ("q_stride", ct.c_int64), ("k_stride", ct.c_int64),
+                ("v_stride", ct.c_int64), ("scale", ct.c_double), ("drop_p", ct.c_double)]
+
+
+class EgnnBiasDesc(ct.Structure):
+    _fields_ = [("n_buckets", ct.c_int32), ("n_columns", ct.c_int32)]
+
+
+class EgnnDropoutDesc(ct.Structure):
+    _fields_ = [("lmax", ct.c_int32), ("C", ct.c_int32), ("share", ct.c_int32), ("storage", ct.c_int32),
+                ("site", ct.c_uint32), ("p", ct.c_double)]
+
+
 class EgnnTimingEntry(ct.Structure):
     _fields_ = [("name", ct.c_char * 48), ("launches", ct.c_int64), ("total_ms", ct.c_double),
                 ("flops", ct.c_double), ("bytes", ct.c_double)]
@@ -53,6 +69,9 @@ _H = ct.POINTER(EgnnHDesc)
 _PSZ = ct.POINTER(ct.c_size_t)
 _B = ct.POINTER(EgnnBasis)
 _O = ct.POINTER(EgnnOrbitals)
+_A = ct.POINTER(EgnnAttnDesc)
+_BD = ct.POINTER(EgnnBiasDesc)
+_DD = ct.POINTER(EgnnDropoutDesc)
 
 SIGNATURES = {
     "egnn_status_string": (ct.c_char_p, [ct.c_int]),
@@ -71,6 +90,16 @@ SIGNATURES = {
     "egnn_layer_bwd": (ct.c_int, [_L, _G, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "egnn_edge_update_fwd": (ct.c_int, [_L, _G, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "egnn_edge_update_bwd": (ct.c_int, [_L, _G, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "egnn_diff_attention_sizes": (ct.c_int, [_A, _G, _PSZ, _PSZ, _PSZ]),
+    "egnn_diff_attention_fwd": (ct.c_int, [_A, _G, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "egnn_diff_attention_bwd": (ct.c_int, [_A, _G, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                           _sz, _vp]),
+    "egnn_distance_borders": (ct.c_int, [_i32, _i32, _f64, _f64, ct.POINTER(ct.c_float)]),
+    "egnn_distance_bias_fwd": (ct.c_int, [_BD, _G, _vp, _vp, _vp, _vp]),
+    "egnn_distance_bias_workspace": (ct.c_int, [_BD, _G, _PSZ]),
+    "egnn_distance_bias_bwd": (ct.c_int, [_BD, _G, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "egnn_dropout_fwd": (ct.c_int, [_DD, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "egnn_dropout_bwd": (ct.c_int, [_DD, _i64, _vp, _vp, _vp, _vp]),
     "egnn_hblocks_label_rows": (ct.c_int32, [_H]),
     "egnn_hblocks": (ct.c_int, [_H, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "egnn_assemble_bsr": (ct.c_int, [_G, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),

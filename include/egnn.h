@@ -272,6 +272,143 @@ egnn_status egnn_edge_update_bwd(const egnn_layer_desc *d, const egnn_graph *g, 
                                  void *ws, size_t ws_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Differential attention over incoming edges  [Review: attention runs over the
+ * edges directed into a node, which that node owns]
+ *
+ * Multi-head attention of every destination row over its incoming edges, as
+ * the difference of two softmax maps with a learned weight per head:
+ *   l[e,h,s]   = scale <q[d,h,s,:], k[src(e),h,s,:]> + bias[e,h,s],  s = 0, 1
+ *   a[.,h,s]   = softmax of l[.,h,s] over the edges of row d
+ *   w[e,h]     = m[e,h] (a[e,h,0] - lam[h] a[e,h,1])
+ *   out[d,k,c] = sum_e w[e,h(c)] v[src(e),k,c],   h(c) = c / (C / H)
+ * m is dropout of the weights (decision e*H + h; see egnn_dropout_desc for the
+ * generator), 1 everywhere when drop_p is 0.  Rows of v and out are irreps
+ * [K][C], K = (lmax+1)^2; a head owns C / H channels of every component, so
+ * with q and k made of invariants the operator commutes with rotations.
+ * lmax = 0 is attention on plain feature rows.
+ *   q [n_dst][H][2][D], k [n_src][H][2][D], v [n_src][K][C], out [n_dst][K][C]
+ *   in the storage type; q, k, v may have longer rows (q_stride, k_stride,
+ *   v_stride elements apart; 0 = packed), e.g. parts of one projection;
+ *   lam [H], bias [n_edges][H][2] (or NULL) fp32; mask [n_edges] uint8 (or
+ *   NULL), 0 = the edge takes no part.
+ * Reads the graph's row_ptr, src and n_edges (dist, shift and vec may be
+ * NULL).  Rows may be of any length, from none to all edges.  A masked edge,
+ * an edge whose source is outside [0, n_src) and a map whose bias is -inf get
+ * weight 0, and what q.k or v holds there (NaN, infinities) does not come
+ * through; a row with nothing left gives zeros.  Logits and softmax
+ * statistics are fp32; out is rounded once.  Results are bit-identical
+ * between runs.  out must not alias an input.
+ * Limits: H 1..32, D 1..256, C 1..1024 a multiple of H, lmax 0..8; 2^28
+ * edges, 2^21 rows and sources (EGNN_E_UNSUPPORTED beyond).
+ *
+ * saved (NULL for inference) receives what the backward reads; the workspace
+ * is ws_infer bytes without it, ws_train with it (which also serves the
+ * backward).  Both are 16-byte aligned, need no clearing, and belong to the
+ * call until its kernels end.
+ *
+ * egnn_diff_attention_bwd: gradients of <grad_out, out>, all fp32 and
+ * overwritten: grad_q, grad_k, grad_v (packed rows), grad_lam [H], and
+ * grad_bias [n_edges][H][2] (NULL: not wanted; it is the gradient of the
+ * logits, so it can be asked for without a bias; 8-byte aligned).
+ * grad_out [n_dst][K][C] fp32.  saved, the graph and rng are as the forward
+ * had them.  Needs the graph's src_ptr and src_perm.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t lmax;       /* rows of v: K = (lmax+1)^2 components                   */
+  int32_t C;          /* channels per component, a multiple of n_heads          */
+  int32_t n_heads;    /* H                                                      */
+  int32_t head_dim;   /* D, channels of one map of a head's query and key       */
+  int32_t storage;    /* egnn_dtype of q, k, v, out                             */
+  uint32_t site;      /* dropout stream of this call site                       */
+  int64_t q_stride, k_stride, v_stride;  /* elements between rows, 0 = packed   */
+  double scale;       /* of the products, e.g. 1/sqrt(D)                        */
+  double drop_p;      /* dropout of the weights, 0 <= p < 1                     */
+} egnn_attn_desc;
+
+egnn_status egnn_diff_attention_sizes(const egnn_attn_desc *d, const egnn_graph *g, size_t *saved_bytes /*host*/,
+                                      size_t *ws_infer_bytes /*host*/, size_t *ws_train_bytes /*host*/);
+egnn_status egnn_diff_attention_fwd(const egnn_attn_desc *d, const egnn_graph *g, const void *q, const void *k,
+                                    const void *v, const float *lam, const float *bias, const uint8_t *mask,
+                                    const uint64_t *rng, void *out, void *saved, void *ws, size_t ws_bytes,
+                                    hipStream_t stream);
+egnn_status egnn_diff_attention_bwd(const egnn_attn_desc *d, const egnn_graph *g, const void *q, const void *k,
+                                    const void *v, const float *lam, const uint64_t *rng, const void *saved,
+                                    const float *grad_out, float *grad_q, float *grad_k, float *grad_v,
+                                    float *grad_lam, float *grad_bias, void *ws, size_t ws_bytes,
+                                    hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Learned bias by distance buckets
+ *
+ * Relative position bias of attention logits, the position of a source seen
+ * from its destination being the edge's length:
+ *   bucket(r) = number of borders <= r          (0 for r = NaN)
+ *   bias[e][:] = table[bucket(dist[e])][:]
+ * borders [n_buckets - 1] fp32 ascending, table [n_buckets][n_columns] fp32,
+ * bias [n_edges][n_columns] fp32 (n_columns = 2 H for
+ * egnn_diff_attention_fwd).  Reads the graph's dist and n_edges.  Borders
+ * that do not ascend give some bucket of the table, never one outside it.
+ * egnn_distance_bias_bwd: grad_table [n_buckets][n_columns] (overwritten) =
+ * the sum of grad_bias over each bucket's edges, bit-identical between runs;
+ * the workspace (16-byte aligned) comes from the query.
+ * egnn_distance_borders (host) fills borders with the usual split: n_linear
+ * buckets of equal width up to r_linear, then equal ratios up to r_max, the
+ * last bucket taking everything beyond.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t n_buckets;   /* 1..1024 */
+  int32_t n_columns;   /* 1..64   */
+} egnn_bias_desc;
+
+egnn_status egnn_distance_borders(int32_t n_buckets, int32_t n_linear, double r_linear, double r_max,
+                                  float *borders /*host [n_buckets - 1]*/);
+egnn_status egnn_distance_bias_fwd(const egnn_bias_desc *d, const egnn_graph *g, const float *borders,
+                                   const float *table, float *bias, hipStream_t stream);
+egnn_status egnn_distance_bias_workspace(const egnn_bias_desc *d, const egnn_graph *g, size_t *bytes /*host*/);
+egnn_status egnn_distance_bias_bwd(const egnn_bias_desc *d, const egnn_graph *g, const float *borders,
+                                   const float *grad_bias, float *grad_table, void *ws, size_t ws_bytes,
+                                   hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Dropout of irreps from a counter-based generator
+ *
+ *   y = residual + m x,   m = 0 or 1/(1-p),  no mask stored
+ * x, y and residual (NULL: none) are [n_rows][K][C] in the storage type,
+ * K = (lmax+1)^2; y may be x or residual.  A decision is shared by what a
+ * rotation mixes, so the operator commutes with rotations:
+ *   EGNN_DROP_CHANNEL  one per (row, channel),          i = row C + c
+ *   EGNN_DROP_DEGREE   one per (row, degree, channel),  i = (row (lmax+1) + l) C + c
+ *   EGNN_DROP_ROW      one per row (drops whole residual branches),  i = row
+ * (lmax = 0: dropout of plain features, an element at a time.)  A dropped
+ * element is the residual (or 0) whatever x holds there.
+ * Decision i keeps iff draw(i) >= t, t = p 65536 rounded to the nearest
+ * integer, and kept elements are multiplied by 65536 / (65536 - t).  draw(i) =
+ * 16-bit part i % 8 (low half of a word first) of Philox4x32-10 with the
+ * seed's low and high word as key and the counter (i/8 low, i/8 high, step,
+ * site).  rng is device memory, {seed, step} as two 64-bit words of which the
+ * step's low 32 bits count, so that a captured graph draws anew when its
+ * owner writes a new step between replays; it may be NULL when t = 0.  Give
+ * every call site of a network a site of its own.  egnn_dropout_bwd:
+ * grad_x = m grad_y (fp32, in place allowed) with the forward's decisions, as
+ * long as rng still holds what the forward read; the gradient of residual is
+ * grad_y itself.  C 1..4096, lmax 0..8, n_rows < 2^31.
+ * ------------------------------------------------------------------------- */
+typedef enum { EGNN_DROP_CHANNEL = 0, EGNN_DROP_DEGREE = 1, EGNN_DROP_ROW = 2 } egnn_drop_share;
+
+typedef struct {
+  int32_t lmax, C;
+  int32_t share;      /* egnn_drop_share                      */
+  int32_t storage;    /* egnn_dtype of x, residual and y      */
+  uint32_t site;
+  double p;           /* 0 <= p < 1 (after rounding)          */
+} egnn_dropout_desc;
+
+egnn_status egnn_dropout_fwd(const egnn_dropout_desc *d, int64_t n_rows, const void *x, const void *residual,
+                             const uint64_t *rng, void *y, hipStream_t stream);
+egnn_status egnn_dropout_bwd(const egnn_dropout_desc *d, int64_t n_rows, const float *grad_y, const uint64_t *rng,
+                             float *grad_x, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Label -> Matrix: Hamiltonian blocks  [MALOQ Sec. III-B1 Eq. (1), Sec. III-B2]
  *
  * Shells (host list shell_l, each l <= 4; n_orb = sum(2l+1) <= 32).  For

@@ -47,4 +47,8 @@ Modules:
   decode     -- Label -> Matrix: Hamiltonian blocks from irreps
   labels     -- Matrix <-> Label over whole matrices with per-element orbital
                 templates (MALOQ Sec. III-B2)
+  attention  -- differential attention over incoming edges, distance buckets,
+                counter-based dropout; each with its backward (definitions of
+                the operators in include/egnn.h; the generator is the
+                published Philox4x32-10)
 """

@@ -1,0 +1,185 @@
+"""Refusals of the attention, bias and dropout calls (no GPU): invalid arguments come back with a status and a message
+from the C ABI, and as ValueError from the binding, before anything is launched."""
+import ctypes as ct
+import os
+
+import pytest
+import torch
+
+from tests.test_abi import _fake_graph
+
+P = ct.c_void_p(0x1000)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from equivariant_gnn_electronic_amd import _lib
+    if not os.path.exists(_lib.LIB_PATH):
+        from equivariant_gnn_electronic_amd import build
+        build.build(verbose=False)
+    return _lib.load()
+
+
+def _attn(**kw):
+    from equivariant_gnn_electronic_amd import _lib
+    a = dict(lmax=4, C=64, n_heads=8, head_dim=16, storage=0, site=0, q_stride=0, k_stride=0, v_stride=0, scale=0.25,
+             drop_p=0.0)
+    a.update(kw)
+    return _lib.EgnnAttnDesc(*a.values())
+
+
+def _sizes(lib, d, g):
+    s = [ct.c_size_t() for _ in range(3)]
+    return lib.egnn_diff_attention_sizes(ct.byref(d), ct.byref(g), *map(ct.byref, s)), [x.value for x in s]
+
+
+@pytest.mark.parametrize("bad", [dict(lmax=-1), dict(lmax=9), dict(C=0), dict(C=60), dict(C=2048), dict(n_heads=0),
+                                 dict(n_heads=33, C=66), dict(head_dim=0), dict(head_dim=257), dict(storage=2),
+                                 dict(q_stride=255), dict(k_stride=1), dict(v_stride=1599), dict(q_stride=-1),
+                                 dict(scale=float("nan")), dict(scale=float("inf")), dict(drop_p=1.0),
+                                 dict(drop_p=-0.1), dict(drop_p=float("nan")), dict(drop_p=0.99999999)])
+def test_attention_description_rejected(lib, bad):
+    from equivariant_gnn_electronic_amd import _lib
+    assert _sizes(lib, _attn(**bad), _fake_graph(10, 10, 100))[0] == _lib.EGNN_E_ARG
+    assert lib.egnn_last_error()
+
+
+@pytest.mark.parametrize("rows,srcs,edges,status", [(-1, 1, 0, 1), (1, -1, 0, 1), (1, 1, -1, 1), (0, 5, 3, 1), (5, 0, 3, 1),
+                                                    (2**21 + 1, 5, 3, 4), (5, 2**21 + 1, 3, 4), (5, 5, 2**28 + 1, 4),
+                                                    (0, 0, 0, 0), (5, 5, 2**28, 0)])
+def test_attention_graph_sizes(lib, rows, srcs, edges, status):
+    assert _sizes(lib, _attn(), _fake_graph(rows, srcs, edges))[0] == status
+
+
+def test_attention_size_queries(lib):
+    ok, small = _sizes(lib, _attn(), _fake_graph(100, 100, 1000))
+    ok2, large = _sizes(lib, _attn(), _fake_graph(100, 100, 2000))
+    assert ok == 0 and ok2 == 0
+    # per edge and head two logits and a weight, per edge a row index
+    assert abs(large[0] - small[0] - 1000 * (8 * 12 + 4)) < 1024
+    assert large[1] >= large[0] and large[2] > 0
+
+
+def test_attention_call_arguments(lib):
+    from equivariant_gnn_electronic_amd import _lib
+    g, d = _fake_graph(100, 100, 1000), _attn()
+    _, (saved, infer, train) = _sizes(lib, d, g)
+
+    def fwd(d=d, g=g, q=P, k=P, v=P, lam=P, rng=None, out=P, keep=None, ws=P, n=1 << 40):
+        return lib.egnn_diff_attention_fwd(ct.byref(d), ct.byref(g), q, k, v, lam, None, None, rng, out, keep, ws, n,
+                                           None)
+
+    for kw in (dict(q=None), dict(k=None), dict(v=None), dict(lam=None), dict(out=None), dict(ws=ct.c_void_p(0x1008)),
+               dict(keep=ct.c_void_p(0x1004)), dict(d=_attn(drop_p=0.5)),
+               dict(d=_attn(drop_p=0.5), rng=ct.c_void_p(0x1004))):
+        assert fwd(**kw) == _lib.EGNN_E_ARG, kw
+    for f in ("row_ptr", "src"):
+        h = _fake_graph(100, 100, 1000)
+        setattr(h, f, None)
+        assert fwd(g=h) == _lib.EGNN_E_ARG
+    assert fwd(n=infer - 1) == _lib.EGNN_E_WORKSPACE and fwd(ws=None) == _lib.EGNN_E_WORKSPACE
+    assert fwd(g=_fake_graph(0, 5, 0)) == 0      # no rows: nothing to do
+    names = ("grad_q", "grad_k", "grad_v", "grad_lam", "grad_bias")
+
+    def bwd(d=d, g=g, q=P, saved=P, go=P, rng=None, ws=P, n=1 << 40, **kw):
+        outs = [kw.get(x, P) for x in names]
+        return lib.egnn_diff_attention_bwd(ct.byref(d), ct.byref(g), q, P, P, P, rng, saved, go, *outs, ws, n, None)
+
+    for kw in (dict(q=None), dict(saved=None), dict(go=None), dict(grad_q=None), dict(grad_k=None), dict(grad_v=None),
+               dict(grad_lam=None), dict(grad_bias=ct.c_void_p(0x1004)), dict(d=_attn(drop_p=0.5))):
+        assert bwd(**kw) == _lib.EGNN_E_ARG, kw
+    for f in ("row_ptr", "src", "src_ptr", "src_perm"):
+        h = _fake_graph(100, 100, 1000)
+        setattr(h, f, None)
+        assert bwd(g=h) == _lib.EGNN_E_ARG
+    assert bwd(n=16) == _lib.EGNN_E_WORKSPACE
+
+
+def test_bias_arguments(lib):
+    from equivariant_gnn_electronic_amd import _lib
+    g = _fake_graph(1, 1, 100)
+    for b, m in ((0, 1), (1025, 1), (1, 0), (1, 65)):
+        d = _lib.EgnnBiasDesc(b, m)
+        assert lib.egnn_distance_bias_fwd(ct.byref(d), ct.byref(g), P, P, P, None) == _lib.EGNN_E_ARG
+    d = _lib.EgnnBiasDesc(8, 4)
+    n = ct.c_size_t()
+    assert lib.egnn_distance_bias_workspace(ct.byref(d), ct.byref(g), ct.byref(n)) == 0 and n.value >= 8 * 4 * 4
+    assert lib.egnn_distance_bias_bwd(ct.byref(d), ct.byref(g), P, P, P, P, n.value - 1, None) == _lib.EGNN_E_WORKSPACE
+    assert lib.egnn_distance_bias_bwd(ct.byref(d), ct.byref(g), P, None, P, P, n.value, None) == _lib.EGNN_E_ARG
+    assert lib.egnn_distance_bias_fwd(ct.byref(d), ct.byref(g), None, P, P, None) == _lib.EGNN_E_ARG
+    g.dist = None
+    assert lib.egnn_distance_bias_fwd(ct.byref(d), ct.byref(g), P, P, P, None) == _lib.EGNN_E_ARG
+
+
+def test_borders(lib):
+    import equivariant_gnn_electronic_amd as eg
+    b = eg.egnn_distance_borders(8, 4, 2.0, 8.0).tolist()
+    # widths of 0.5 up to 2, then ratios of sqrt(2) up to the last border 2 * 4^(3/4)
+    assert b == pytest.approx([0.5, 1.0, 1.5, 2.0, 2 * 2 ** 0.5, 4.0, 4 * 2 ** 0.5], rel=2 ** -23)
+    assert eg.egnn_distance_borders(1, 1, 1.0, 2.0).numel() == 0
+    assert eg.egnn_distance_borders(3, 3, 3.0, 3.0).tolist() == [1.0, 2.0]
+    for bad in ((0, 1, 1, 2), (1025, 1, 1, 2), (4, 0, 1, 2), (4, 5, 1, 2), (4, 2, 0, 2), (4, 2, 2, 2),
+                (4, 2, float("nan"), 2), (4, 2, 1, float("inf"))):
+        with pytest.raises(eg.EgnnError):
+            eg.egnn_distance_borders(*bad)
+
+
+@pytest.mark.parametrize("bad", [dict(lmax=-1), dict(lmax=9), dict(C=0), dict(C=4097), dict(share=3), dict(storage=5),
+                                 dict(p=1.0), dict(p=-1e-3), dict(p=float("nan")), dict(p=0.9999999)])
+def test_dropout_description_rejected(lib, bad):
+    from equivariant_gnn_electronic_amd import _lib
+    a = dict(lmax=1, C=8, share=0, storage=0, site=0, p=0.1)
+    a.update(bad)
+    d = _lib.EgnnDropoutDesc(*a.values())
+    assert lib.egnn_dropout_fwd(ct.byref(d), 4, P, None, P, P, None) == _lib.EGNN_E_ARG
+    assert lib.egnn_dropout_bwd(ct.byref(d), 4, P, P, P, None) == _lib.EGNN_E_ARG
+
+
+def test_dropout_call_arguments(lib):
+    from equivariant_gnn_electronic_amd import _lib
+    d = _lib.EgnnDropoutDesc(1, 8, 0, 0, 0, 0.1)
+    for n, x, rng, y in ((4, None, P, P), (4, P, None, P), (4, P, P, None), (4, P, ct.c_void_p(0x1004), P), (-1, P, P, P),
+                         (2**31, P, P, P)):
+        assert lib.egnn_dropout_fwd(ct.byref(d), n, x, None, rng, y, None) == _lib.EGNN_E_ARG
+    assert lib.egnn_dropout_fwd(ct.byref(d), 0, None, None, None, None, None) == 0
+
+
+def test_binding_checks_tensors_before_the_device():
+    import equivariant_gnn_electronic_amd as eg
+    g = eg.Graph.from_csr(torch.tensor([0, 2, 3], dtype=torch.int32), torch.zeros(3, dtype=torch.int32), n_src=2)
+    g.dist = torch.ones(3)
+    d = eg.attn_desc(1, 8, 2, 4)
+    q, v, lam = torch.zeros(2, 2, 2, 4), torch.zeros(2, 4, 8), torch.zeros(2)
+
+    def call(**kw):
+        a = dict(q=q, k=q, v=v, lam=lam, desc=d)
+        opt = {n: kw.pop(n) for n in ("bias", "mask", "rng", "out") if n in kw}
+        a.update(kw)
+        return eg.egnn_diff_attention_fwd(a["desc"], g, a["q"], a["k"], a["v"], a["lam"], **opt)
+
+    for kw, text in ((dict(q=q.bfloat16()), "q must be"), (dict(q=q[:1]), "at least 2 rows"),
+                     (dict(k=torch.zeros(2, 2, 4, 2)), "k must have shape"), (dict(v=v.transpose(1, 2)), "v must have shape"),
+                     (dict(v=torch.zeros(2, 8, 4).transpose(1, 2)), "must be packed"),
+                     (dict(q=q[:1].expand(2, 2, 2, 4)), "overlap"), (dict(lam=torch.zeros(3)), "lam must have shape"),
+                     (dict(bias=torch.zeros(3, 3)), "bias must have shape"), (dict(mask=torch.ones(2, dtype=torch.bool)), "mask"),
+                     (dict(mask=torch.ones(3)), "mask must be"), (dict(desc=eg.attn_desc(1, 8, 2, 4, drop_p=0.1)), "rng"),
+                     (dict(rng=torch.zeros(2)), "rng must be"), (dict(q=None), "torch tensor"), ({}, "must live on the GPU")):
+        with pytest.raises(ValueError, match=text):
+            call(**kw)
+    with pytest.raises(ValueError, match="grouped by source"):
+        eg.egnn_diff_attention_bwd(d, g, q, q, v, lam, None, v)
+    with pytest.raises(ValueError, match="borders must have shape"):
+        eg.egnn_distance_bias_fwd(g, torch.zeros(3), torch.zeros(5, 4))
+    with pytest.raises(ValueError, match="must live on the GPU"):
+        eg.egnn_distance_bias_fwd(g, torch.zeros(4), torch.zeros(5, 4))
+    with pytest.raises(ValueError, match="grad_bias must have"):
+        eg.egnn_distance_bias_bwd(g, torch.zeros(4), torch.zeros(2, 4))
+    with pytest.raises(ValueError, match="unknown sharing"):
+        eg.dropout_desc(0, 8, 0.1, share="head")
+    dd = eg.dropout_desc(0, 8, 0.1)
+    state = torch.zeros(2, dtype=torch.int64)
+    for x, r, text in ((torch.zeros(3, 8), state, "dimensions"), (torch.zeros(3, 1, 8), None, "rng"),
+                       (torch.zeros(3, 1, 8, dtype=torch.float64), state, "x must be"),
+                       (torch.zeros(3, 1, 8), state, "must live on the GPU")):
+        with pytest.raises(ValueError, match=text):
+            eg.egnn_dropout_fwd(dd, x, r)

@@ -88,6 +88,8 @@ template <> struct Vec<uint16_t, 8> {
   }
 };
 
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // Edges [b, e) of row d; bounds from memory are held inside [0, E].
 __device__ inline void row_bounds(const int *ptr, int d, int E, int *b, int *e) {
   const int lo = min(max(ptr[d], 0), E);
@@ -215,17 +217,49 @@ inline Team make_team(int H, int vectors) {
   return t;
 }
 
-// lds[i * H + h] = sum over the head's vectors of A . B[col[b + i]], i < cnt.
-// A stays in registers, NIT vectors a lane.
-// Head h's vector j lies at (j / P) C + h Ch + (j % P) VW.
-template <typename TA, typename TB, int VW, int NIT>
-__device__ inline void edge_dots(const TA *arow, const TB *B, int64_t ldb, const int *col, int n_col, int b, int cnt,
-                                 int H, int C, int Ch, int nvec, Team tm, float *lds) {
+template <int CTRL> __device__ inline float dpp_move(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+
+// dot[u] summed over teams of 2^LTl lanes; every lane of a team gets the sum.
+// Up to 16 lanes the steps are DPP moves inside a row of 16 (a quad's lanes
+// hold the same value when the mirrors swap quads), no LDS permutes.
+template <int U>
+__device__ inline void team_sum(float (&dot)[U], int LTl) {
+  if (LTl > 0)
+#pragma unroll
+    for (int u = 0; u < U; ++u) dot[u] += dpp_move<0xB1>(dot[u]);   // quad [1,0,3,2]
+  if (LTl > 1)
+#pragma unroll
+    for (int u = 0; u < U; ++u) dot[u] += dpp_move<0x4E>(dot[u]);   // quad [2,3,0,1]
+  if (LTl > 2)
+#pragma unroll
+    for (int u = 0; u < U; ++u) dot[u] += dpp_move<0x141>(dot[u]);  // mirror within 8
+  if (LTl > 3)
+#pragma unroll
+    for (int u = 0; u < U; ++u) dot[u] += dpp_move<0x140>(dot[u]);  // mirror within 16
+  if (LTl > 4)
+#pragma unroll
+    for (int u = 0; u < U; ++u) dot[u] += __shfl_xor(dot[u], 16);
+  if (LTl > 5)
+#pragma unroll
+    for (int u = 0; u < U; ++u) dot[u] += __shfl_xor(dot[u], 32);
+}
+
+// lds[i * H + h] = sum over the head's vectors of A . B[scol[i]], i < cnt.
+// A stays in registers, NIT vectors a lane.  Head h's vector j lies at
+// (j / P) C + h Ch + (j % P) VW.  ONE: a wave takes one edge at a time (teams
+// fill it), so the row's address is scalar work and the loads are scalar base
+// plus the lane's fixed offset.
+template <typename TA, typename TB, int VW, int NIT, bool ONE>
+__device__ inline void edge_dots(const TA *arow, const TB *B, int64_t ldb, const int *scol, int cnt, int H, int C,
+                                 int Ch, int nvec, Team tm, float *lds) {
   constexpr int U = NIT >= 8 ? 1 : 8 / NIT;  // eight loads in flight
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x >> 6);
   const int LT = 1 << tm.LTl;
-  const int t = lane & (LT - 1), hh = (lane >> tm.LTl) & ((1 << tm.Hpl) - 1), es = lane >> (tm.LTl + tm.Hpl);
-  const int EPW = kWave >> (tm.LTl + tm.Hpl);
+  const int t = lane & (LT - 1), hh = (lane >> tm.LTl) & ((1 << tm.Hpl) - 1);
+  const int es = ONE ? 0 : lane >> (tm.LTl + tm.Hpl);
+  const int EPW = ONE ? 1 : kWave >> (tm.LTl + tm.Hpl);
   const int h = min(hh, H - 1);
   const int P = Ch / VW;
   for (int c0 = 0; c0 < nvec; c0 += LT * NIT) {
@@ -241,30 +275,42 @@ __device__ inline void edge_dots(const TA *arow, const TB *B, int64_t ldb, const
       Vec<TA, VW>::ld(arow + off[i], af[i]);
     }
     for (int i0 = wave * EPW; i0 < cnt; i0 += kWaves * EPW * U) {
-      float v[U][NIT][VW];
+      float v[U][NIT][VW], dot[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * kWaves * EPW + es;
-        const int s = col[b + min(i, cnt - 1)];
-        const TB *row = B + static_cast<int64_t>(static_cast<unsigned>(s) < static_cast<unsigned>(n_col) ? s : 0) * ldb;
+        const int i = min(i0 + u * kWaves * EPW + es, cnt - 1);
+        const int s = ONE ? uniform(scol[i]) : scol[i];
+        const TB *row = B + static_cast<int64_t>(s) * ldb;
 #pragma unroll
         for (int n = 0; n < NIT; ++n) Vec<TB, VW>::ld(row + off[n], v[u][n]);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * kWaves * EPW + es;
-        float dot = 0.0f;
+        dot[u] = 0.0f;
 #pragma unroll
         for (int n = 0; n < NIT; ++n) {
           float part = 0.0f;
 #pragma unroll
           for (int x = 0; x < VW; ++x) part += af[n][x] * v[u][n][x];
-          dot += ok[n] ? part : 0.0f;
+          dot[u] += ok[n] ? part : 0.0f;
         }
-        for (int o = 1; o < LT; o <<= 1) dot += __shfl_xor(dot, o);
-        if (t == 0 && hh < H && i < cnt) lds[i * H + hh] = c0 == 0 ? dot : lds[i * H + hh] + dot;
+      }
+      team_sum<U>(dot, tm.LTl);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * kWaves * EPW + es;
+        if (t == 0 && hh < H && i < cnt) lds[i * H + hh] = c0 == 0 ? dot[u] : lds[i * H + hh] + dot[u];
       }
     }
+  }
+}
+
+// The source of each of cnt edges, sources outside the list as row 0 (their
+// logits are masked).
+__device__ inline void stage_sources(const int *src, int b, int cnt, int n_src, int *scol) {
+  for (int i = threadIdx.x; i < cnt; i += kThreads) {
+    const int s = src[b + i];
+    scol[i] = static_cast<unsigned>(s) < static_cast<unsigned>(n_src) ? s : 0;
   }
 }
 
@@ -287,10 +333,11 @@ struct LogitArgs {
 
 // One block per row (or piece): logits, softmax statistics and, for whole
 // rows, the edge weights.
-template <typename T, int VW, int NIT>
+template <typename T, int VW, int NIT, bool ONE>
 __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *__restrict__ q,
                                                           const T *__restrict__ k) {
-  extern __shared__ float lg[];  // [T][2H]
+  extern __shared__ float lg[];  // [T][2H], then the sources [T]
+  int *scol = reinterpret_cast<int *>(lg + a.T * 2 * a.H);
   __shared__ float red[kWaves][kWave];
   __shared__ float2 fin[kWave];
   const int H2 = 2 * a.H;
@@ -310,8 +357,10 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *
   }
   const int cnt = e - b;
   for (int i = threadIdx.x; i < cnt; i += kThreads) a.dst[b + i] = d;
-  edge_dots<T, T, VW, NIT>(q + static_cast<int64_t>(d) * a.ldq, k, a.ldk, a.src, a.n_src, b, cnt, H2, H2 * a.D, a.D,
-                           a.D / VW, a.team, lg);
+  stage_sources(a.src, b, cnt, a.n_src, scol);
+  __syncthreads();
+  edge_dots<T, T, VW, NIT, ONE>(q + static_cast<int64_t>(d) * a.ldq, k, a.ldk, scol, cnt, H2, H2 * a.D, a.D, a.D / VW,
+                                a.team, lg);
   __syncthreads();
   const int Hp = 1 << a.team.Hpl;
   const int col = threadIdx.x & (Hp - 1), r0 = threadIdx.x >> a.team.Hpl, R = kThreads >> a.team.Hpl;
@@ -412,10 +461,11 @@ __device__ inline void logit_grads(const GradArgs &a, int64_t o, int h, float u,
 
 // One block per row (or piece): u = m <grad_out, v> per edge and head, then the
 // softmax's backward for both maps.
-template <typename T, int VW, int NIT>
+template <typename T, int VW, int NIT, bool ONE>
 __global__ void __launch_bounds__(kThreads) logit_grad_kernel(GradArgs a, const float *__restrict__ go,
                                                               const T *__restrict__ v) {
-  extern __shared__ float us[];  // [T][H]
+  extern __shared__ float us[];  // [T][H], then the sources [T]
+  int *scol = reinterpret_cast<int *>(us + a.T * a.H);
   __shared__ float red[kWaves][kWave];
   __shared__ float4 st[kMaxHeads];
   __shared__ float2 tt[kMaxHeads];
@@ -440,8 +490,10 @@ __global__ void __launch_bounds__(kThreads) logit_grad_kernel(GradArgs a, const 
   if (threadIdx.x < static_cast<unsigned>(H))
     st[threadIdx.x] = reinterpret_cast<const float4 *>(a.stats)[static_cast<int64_t>(d) * H + threadIdx.x];
   const int Ch = a.C / H;
-  edge_dots<float, T, VW, NIT>(go + static_cast<int64_t>(d) * a.K * a.C, v, a.ldv, a.src, a.n_src, b, cnt, H, a.C, Ch,
-                               a.K * (Ch / VW), a.team, us);
+  stage_sources(a.src, b, cnt, a.n_src, scol);
+  __syncthreads();
+  edge_dots<float, T, VW, NIT, ONE>(go + static_cast<int64_t>(d) * a.K * a.C, v, a.ldv, scol, cnt, H, a.C, Ch,
+                                    a.K * (Ch / VW), a.team, us);
   __syncthreads();
   for_decisions(b, cnt, H, a.drop, [&](int at, int, int, float m) {
     const float x = m == 0.0f ? 0.0f : m * us[at];
@@ -539,17 +591,122 @@ struct SumArgs {
   const float *w;       // [E][H]
   int H, C, Ch, width;  // out row = width elements; column c of width has head (c % C) / Ch
   int S, SV, Gl;        // slices, vectors a slice, log2 of lanes an edge
+  int BE;               // edges staged at a time
   int unit0, units, blocks;  // first unit of the launch; rows + pieces; blocks a slice in the launch
   float scale;
   float *part;          // [pieces][width]
 };
 
+constexpr int kStage = 1024;  // weights a wave stages at a time (4 KB)
+
+template <bool PERM> __device__ inline int owner(const SumArgs &a, int pos) {
+  if constexpr (PERM) {
+    const int ed = a.perm[pos];
+    return static_cast<unsigned>(ed) < static_cast<unsigned>(a.E) ? a.row_of[ed] : -1;
+  }
+  return a.row_of[pos];
+}
+
+// The next BE edges of a list: lane i < BE holds edge j0 + i's row of X, and
+// the lanes together the BE x H weights, four a register where H allows.
+// Edges past the end and rows outside X have weight 0 and row 0.
+template <bool PERM, bool W4> struct Batch {
+  int x;
+  float4 w4[kStage / 4 / kWave];
+  float w1[kStage / kWave];
+
+  __device__ inline void fetch(const SumArgs &a, int j0, int e, int lane) {
+    int ed = -1;
+    x = 0;
+    if (lane < a.BE && j0 + lane < e) {
+      ed = PERM ? a.perm[j0 + lane] : j0 + lane;
+      if (PERM && static_cast<unsigned>(ed) >= static_cast<unsigned>(a.E)) ed = -1;
+      if (ed >= 0) {
+        const int s = a.col[ed];
+        if (static_cast<unsigned>(s) < static_cast<unsigned>(a.n_x)) x = s;
+        else ed = -1;
+      }
+    }
+    const int per = W4 ? a.H / 4 : a.H, n = a.BE * per;
+#pragma unroll
+    for (int t = 0; t < (W4 ? kStage / 4 / kWave : kStage / kWave); ++t) {
+      const int f = t * kWave + lane;
+      if (t * kWave >= n) break;
+      const int i = f / per;
+      const int from = __shfl(ed, i & (kWave - 1));
+      const bool live = f < n && from >= 0;
+      const int64_t at = static_cast<int64_t>(from) * a.H + (f - i * per) * (W4 ? 4 : 1);
+      if constexpr (W4)
+        w4[t] = live ? *reinterpret_cast<const float4 *>(a.w + at) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      else
+        w1[t] = live ? a.w[at] : 0.0f;
+    }
+  }
+
+  __device__ inline void stage(const SumArgs &a, int lane, float *sw, int *sx) const {
+    const int n = a.BE * (W4 ? a.H / 4 : a.H);
+#pragma unroll
+    for (int t = 0; t < (W4 ? kStage / 4 / kWave : kStage / kWave); ++t) {
+      const int f = t * kWave + lane;
+      if (t * kWave >= n) break;
+      if (f < n) {
+        if constexpr (W4) reinterpret_cast<float4 *>(sw)[f] = w4[t];
+        else sw[f] = w1[t];
+      }
+    }
+    sx[lane] = x;
+  }
+};
+
+// acc += sum over edges [b, e) of w X.  ONE: the whole wave takes one edge at
+// a time and its row's address is scalar work; else 64 >> Gl edges at once.
+// SAFE skips weights of 0, so that what such a row of X holds stays out.
+template <typename TX, int VW, bool PERM, bool ONE, bool W4, bool SAFE>
+__device__ inline void gather_rows(const SumArgs &a, const TX *X, int b, int e, int c, int head, int lane, float *sw,
+                                   int *sx, float (&acc)[VW]) {
+  constexpr int U = 8;
+  const int grp = ONE ? 0 : lane >> a.Gl, EPW = ONE ? 1 : kWave >> a.Gl;
+  Batch<PERM, W4> next;
+  next.fetch(a, b, e, lane);
+  for (int j0 = b; j0 < e; j0 += a.BE) {
+    next.stage(a, lane, sw, sx);
+    const int x = next.x;
+    wave_lds_order();
+    if (j0 + a.BE < e) next.fetch(a, j0 + a.BE, e, lane);  // under way while this batch is summed
+    const int n = min(a.BE, e - j0);
+    for (int i0 = 0; i0 < n; i0 += EPW * U) {
+      float v[U][VW], w[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        int i, s;
+        if constexpr (ONE) {
+          i = i0 + u;
+          s = __builtin_amdgcn_readlane(x, i);
+        } else {
+          i = min(i0 + u * EPW + grp, a.BE - 1);
+          s = sx[i];
+        }
+        w[u] = sw[i * a.H + head];
+        if constexpr (!ONE)
+          if (i0 + u * EPW + grp >= a.BE) w[u] = 0.0f;
+        Vec<TX, VW>::ld(X + static_cast<int64_t>(s) * a.ldx + c, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < VW; ++k) acc[k] = fmaf(w[u], SAFE && w[u] == 0.0f ? 0.0f : v[u][k], acc[k]);
+    }
+    wave_lds_order();
+  }
+}
+
 // out[r] = scale sum over the row's edges of w[e][head] X[col[e]].  One wave
-// per (row or piece, slice of columns); 64 >> Gl edges at a time.
-template <typename TX, typename TO, int VW, bool PERM>
+// per (row or piece, slice of columns).
+template <typename TX, typename TO, int VW, bool PERM, bool ONE, bool W4>
 __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const TX *__restrict__ X,
                                                               TO *__restrict__ out) {
-  constexpr int U = 8;
+  __shared__ __align__(16) float sw[kWaves][kStage];
+  __shared__ int sx[kWaves][kWave];
   // consecutive blocks go to the eight XCDs in turn: a slice stays on one XCD
   // (S a multiple of 8), so each L2 holds an eighth of X
   int slice, rb;
@@ -561,8 +718,8 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const T
     slice = (qd / a.blocks) * 8 + (blockIdx.x & 7);
     rb = qd % a.blocks;
   }
-  const int lane = threadIdx.x & (kWave - 1);
-  const int unit = a.unit0 + rb * kWaves + static_cast<int>(threadIdx.x >> 6);
+  const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x >> 6);
+  const int unit = a.unit0 + rb * kWaves + wave;
   if (unit >= a.units) return;
   int row, b, e;
   const int p = unit - a.n_rows;
@@ -571,19 +728,15 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const T
     row_bounds(a.ptr, row, a.E, &b, &e);
     if (e - b > a.T) return;
   } else {
-    const Piece pc = find_piece(p, a.T, a.ptr, a.n_rows, a.E, [&](int pos) {
-      if constexpr (PERM) {
-        const int ed = a.perm[pos];
-        return static_cast<unsigned>(ed) < static_cast<unsigned>(a.E) ? a.row_of[ed] : -1;
-      }
-      return a.row_of[pos];
-    });
+    const Piece pc = find_piece(p, a.T, a.ptr, a.n_rows, a.E, [&](int pos) { return owner<PERM>(a, pos); });
     if (pc.row < 0) return;
     row = pc.row;
     b = pc.begin;
     e = pc.end;
   }
-  const int G = 1 << a.Gl, gl = lane & (G - 1), grp = lane >> a.Gl, EPW = kWave >> a.Gl;
+  b = uniform(b);
+  e = uniform(e);
+  const int gl = ONE ? lane : lane & ((1 << a.Gl) - 1);
   const int nv = a.width / VW;
   const int vj = slice * a.SV + gl;
   const bool on = gl < a.SV && vj < nv;
@@ -591,50 +744,44 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const T
   const int head = (c % a.C) / a.Ch;
   float acc[VW];
 #pragma unroll
-  for (int x = 0; x < VW; ++x) acc[x] = 0.0f;
-  for (int j0 = b; j0 < e; j0 += EPW * U) {
-    float v[U][VW], w[U];
+  for (int k = 0; k < VW; ++k) acc[k] = 0.0f;
+  gather_rows<TX, VW, PERM, ONE, W4, false>(a, X, b, e, c, head, lane, sw[wave], sx[wave], acc);
+  // A sum that is finite had no infinity or NaN in it, so its weights of 0
+  // added 0.  One that is not is taken again with those edges left out.
+  bool odd = false;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * EPW + grp;
-      int ed = min(j, e - 1);
-      bool live = j < e;
-      if constexpr (PERM) {
-        ed = a.perm[ed];
-        live = live && static_cast<unsigned>(ed) < static_cast<unsigned>(a.E);
-        if (!live) ed = 0;
-      }
-      int s = a.col[ed];
-      live = live && static_cast<unsigned>(s) < static_cast<unsigned>(a.n_x);
-      if (!live) s = 0;
-      w[u] = live ? a.w[static_cast<int64_t>(ed) * a.H + head] : 0.0f;
-      Vec<TX, VW>::ld(X + static_cast<int64_t>(s) * a.ldx + c, v[u]);
-    }
+  for (int k = 0; k < VW; ++k) odd = odd || !(fabsf(acc[k]) < INFINITY);
+  if (__any(odd)) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int x = 0; x < VW; ++x) acc[x] += w[u] == 0.0f ? 0.0f : w[u] * v[u][x];  // a weight of 0 hides NaN and inf
+    for (int k = 0; k < VW; ++k) acc[k] = 0.0f;
+    gather_rows<TX, VW, PERM, ONE, W4, true>(a, X, b, e, c, head, lane, sw[wave], sx[wave], acc);
   }
-  for (int o = G; o < kWave; o <<= 1)
+  if constexpr (!ONE)
+    for (int o = 1 << a.Gl; o < kWave; o <<= 1)
 #pragma unroll
-    for (int x = 0; x < VW; ++x) acc[x] += __shfl_xor(acc[x], o);
-  if (grp != 0 || !on) return;
+      for (int k = 0; k < VW; ++k) acc[k] += __shfl_xor(acc[k], o);
+  if (!on || (!ONE && (lane >> a.Gl) != 0)) return;
   if (p >= 0) {
     Vec<float, VW>::st(a.part + static_cast<int64_t>(p) * a.width + c, acc);
     return;
   }
 #pragma unroll
-  for (int x = 0; x < VW; ++x) acc[x] *= a.scale;
+  for (int k = 0; k < VW; ++k) acc[k] *= a.scale;
   Vec<TO, VW>::st(out + static_cast<int64_t>(row) * a.width + c, acc);
 }
 
-// Long rows: the pieces' sums, added in edge order.
-template <typename TO>
+// Long rows: the pieces' sums, added in edge order.  One block per window and
+// 256 columns; it acts for the long row that starts in its window, if any.
+template <typename TO, bool PERM>
 __global__ void __launch_bounds__(kThreads) long_sum_kernel(SumArgs a, TO *__restrict__ out) {
+  const int total = min(max(a.ptr[a.n_rows], 0), a.E);
+  const int64_t w0 = static_cast<int64_t>(blockIdx.x) * a.T;
+  if (w0 >= total) return;
+  const int row = owner<PERM>(a, static_cast<int>(min(w0 + a.T, static_cast<int64_t>(total)) - 1));
+  if (row < 0 || row >= a.n_rows) return;
   int b, e;
-  const int row = a.unit0 + static_cast<int>(blockIdx.x);
   row_bounds(a.ptr, row, a.E, &b, &e);
-  if (e - b <= a.T) return;
+  if (e - b <= a.T || b < w0) return;
   const int c = blockIdx.y * kThreads + threadIdx.x;
   if (c >= a.width) return;
   const int n = piece_count(b, e, a.T);
@@ -778,6 +925,17 @@ size_t ws_bwd_of(const Shape &s) {
 }
 
 template <typename TX, typename TO, bool PERM>
+void launch_sum(unsigned grid, bool vec, bool one, bool w4, hipStream_t st, const SumArgs &a, const TX *X, TO *out) {
+  constexpr int V = 16 / sizeof(TX);
+  if (vec && one && w4) gather_sum_kernel<TX, TO, V, PERM, true, true><<<grid, kThreads, 0, st>>>(a, X, out);
+  else if (vec && one) gather_sum_kernel<TX, TO, V, PERM, true, false><<<grid, kThreads, 0, st>>>(a, X, out);
+  else if (vec && w4) gather_sum_kernel<TX, TO, V, PERM, false, true><<<grid, kThreads, 0, st>>>(a, X, out);
+  else if (vec) gather_sum_kernel<TX, TO, V, PERM, false, false><<<grid, kThreads, 0, st>>>(a, X, out);
+  else if (one) gather_sum_kernel<TX, TO, 1, PERM, true, false><<<grid, kThreads, 0, st>>>(a, X, out);
+  else gather_sum_kernel<TX, TO, 1, PERM, false, false><<<grid, kThreads, 0, st>>>(a, X, out);
+}
+
+template <typename TX, typename TO, bool PERM>
 egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream_t st) {
   if (a.n_rows == 0) return EGNN_OK;
   const int vw = vec_width<TX>(a.Ch, a.ldx, X) > 1 && aligned16(out) ? 16 / sizeof(TX) : 1;
@@ -787,7 +945,7 @@ egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream
   a.Gl = p.Gl;
   a.T = p.T;
   a.units = static_cast<int>(a.n_rows + p.pieces);
-  constexpr int V = 16 / sizeof(TX);
+  a.BE = a.H <= kStage / kWave ? kWave : kStage / kMaxHeads / 2;
   const int most = kMaxBlocks / a.S;  // blocks a slice in one launch
   for (a.unit0 = 0; a.unit0 < a.units; a.unit0 += most * kWaves) {
     Timed t(st, name, a.unit0 ? 0.0 : 2.0 * a.E * a.width,
@@ -797,36 +955,31 @@ egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream
     const int left = (a.units - a.unit0 + kWaves - 1) / kWaves;
     a.blocks = left < most ? left : most;
     const unsigned grid = static_cast<unsigned>(a.blocks) * a.S;
-    if (vw > 1)
-      gather_sum_kernel<TX, TO, V, PERM><<<grid, kThreads, 0, st>>>(a, X, out);
-    else
-      gather_sum_kernel<TX, TO, 1, PERM><<<grid, kThreads, 0, st>>>(a, X, out);
+    launch_sum<TX, TO, PERM>(grid, vw > 1, p.Gl == 6, a.H % 4 == 0 && aligned16(a.w), st, a, X, out);
     EGNN_CHECK_LAUNCH();
   }
   if (p.pieces) {
     Timed t(st, "attn_long_sum", 0.0, 0.0);
-    for (a.unit0 = 0; a.unit0 < a.n_rows; a.unit0 += kMaxBlocks) {
-      const int n = a.n_rows - a.unit0 < kMaxBlocks ? a.n_rows - a.unit0 : kMaxBlocks;
-      long_sum_kernel<TO><<<dim3(n, ceil_div(a.width, kThreads)), kThreads, 0, st>>>(a, out);
-      EGNN_CHECK_LAUNCH();
-    }
+    long_sum_kernel<TO, PERM><<<dim3(static_cast<unsigned>(p.pieces / 2), ceil_div(a.width, kThreads)), kThreads, 0,
+                                st>>>(a, out);
+    EGNN_CHECK_LAUNCH();
   }
   return EGNN_OK;
 }
 
-template <typename T, int VW>
+template <typename T, int VW, bool ONE>
 void launch_logits(unsigned grid, size_t lds, int nit, hipStream_t st, const LogitArgs &a, const T *q, const T *k) {
-  if (nit <= 1) logits_kernel<T, VW, 1><<<grid, kThreads, lds, st>>>(a, q, k);
-  else if (nit <= 2) logits_kernel<T, VW, 2><<<grid, kThreads, lds, st>>>(a, q, k);
-  else logits_kernel<T, VW, 4><<<grid, kThreads, lds, st>>>(a, q, k);
+  if (nit <= 1) logits_kernel<T, VW, 1, ONE><<<grid, kThreads, lds, st>>>(a, q, k);
+  else if (nit <= 2) logits_kernel<T, VW, 2, ONE><<<grid, kThreads, lds, st>>>(a, q, k);
+  else logits_kernel<T, VW, 4, ONE><<<grid, kThreads, lds, st>>>(a, q, k);
 }
 
-template <typename T, int VW>
+template <typename T, int VW, bool ONE>
 void launch_logit_grad(unsigned grid, size_t lds, int nit, hipStream_t st, const GradArgs &a, const float *go,
                        const T *v) {
-  if (nit <= 1) logit_grad_kernel<T, VW, 1><<<grid, kThreads, lds, st>>>(a, go, v);
-  else if (nit <= 4) logit_grad_kernel<T, VW, 4><<<grid, kThreads, lds, st>>>(a, go, v);
-  else logit_grad_kernel<T, VW, 8><<<grid, kThreads, lds, st>>>(a, go, v);
+  if (nit <= 1) logit_grad_kernel<T, VW, 1, ONE><<<grid, kThreads, lds, st>>>(a, go, v);
+  else if (nit <= 4) logit_grad_kernel<T, VW, 4, ONE><<<grid, kThreads, lds, st>>>(a, go, v);
+  else logit_grad_kernel<T, VW, 8, ONE><<<grid, kThreads, lds, st>>>(a, go, v);
 }
 
 int rounds_of(int vectors, const Team &t) {
@@ -871,13 +1024,16 @@ egnn_status forward(const Shape &s, const egnn_graph *g, const T *q, const T *k,
     const int vectors = vec ? s.D / V : s.D;
     a.team = make_team(2 * s.H, vectors);
     const unsigned grid = static_cast<unsigned>(s.n_dst + s.pieces);
-    const size_t lds = static_cast<size_t>(s.T) * 2 * s.H * 4;
+    const size_t lds = static_cast<size_t>(s.T) * (2 * s.H + 1) * 4;
     {
       Timed t(st, "attn_logits", 4.0 * s.E * s.H * s.D,
               static_cast<double>(s.E) * (12.0 * s.H + 8 + (bias ? 8.0 * s.H : 0)) +
                   2.0 * s.H * s.D * sizeof(T) * (static_cast<double>(s.n_dst) + s.n_src));
-      if (vec) launch_logits<T, V>(grid, lds, rounds_of(vectors, a.team), st, a, q, k);
-      else launch_logits<T, 1>(grid, lds, rounds_of(vectors, a.team), st, a, q, k);
+      const int nit = rounds_of(vectors, a.team);
+      const bool one = a.team.LTl + a.team.Hpl == 6;
+      if (vec && one) launch_logits<T, V, true>(grid, lds, nit, st, a, q, k);
+      else if (vec) launch_logits<T, V, false>(grid, lds, nit, st, a, q, k);
+      else launch_logits<T, 1, false>(grid, lds, nit, st, a, q, k);
       EGNN_CHECK_LAUNCH();
     }
     if (s.pieces) {
@@ -950,13 +1106,16 @@ egnn_status backward(const Shape &s, const egnn_graph *g, const T *q, const T *k
     const int vectors = s.K * (vec ? Ch / V : Ch);
     a.team = make_team(s.H, vectors);
     const unsigned grid = static_cast<unsigned>(s.n_dst + s.pieces);
-    const size_t lds = static_cast<size_t>(s.T) * s.H * 4;
+    const size_t lds = static_cast<size_t>(s.T) * (s.H + 1) * 4;
     {
       Timed t(st, "attn_logit_grad", 2.0 * s.E * s.K * s.C,
               static_cast<double>(s.E) * (16.0 * s.H + 4) +
                   static_cast<double>(s.K) * s.C * (4.0 * s.n_dst + sizeof(T) * static_cast<double>(s.n_src)));
-      if (vec) launch_logit_grad<T, V>(grid, lds, rounds_of(vectors, a.team), st, a, go, v);
-      else launch_logit_grad<T, 1>(grid, lds, rounds_of(vectors, a.team), st, a, go, v);
+      const int nit = rounds_of(vectors, a.team);
+      const bool one = a.team.LTl + a.team.Hpl == 6;
+      if (vec && one) launch_logit_grad<T, V, true>(grid, lds, nit, st, a, go, v);
+      else if (vec) launch_logit_grad<T, V, false>(grid, lds, nit, st, a, go, v);
+      else launch_logit_grad<T, 1, false>(grid, lds, nit, st, a, go, v);
       EGNN_CHECK_LAUNCH();
     }
     if (s.pieces) {

@@ -37,6 +37,10 @@ constexpr int kMaxHeads = 32;
 constexpr int kMaxBlocks = 1 << 22;        // of a launch: its threads are counted in 32 bits
 constexpr int64_t kMaxEdges = 1 << 28;     // at most 2^23 pieces of 64 edges or more
 constexpr int kMaxRows = kMaxBlocks / 2;
+constexpr int64_t kMaxStride = 1 << 29;    // a row's pitch in bytes is counted in 32 bits
+constexpr int64_t kSliceBytes = 3200000;   // of X in one XCD's L2
+constexpr int64_t kPartBytes = 3600000;    // of v in one XCD's L2 (dot products)
+constexpr int kMinSlice = 16;              // vectors of the narrowest slice
 
 // ------------------------------------------------------------------ helpers
 
@@ -89,6 +93,39 @@ template <> struct Vec<uint16_t, 8> {
 };
 
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// A byte offset the wave shares, kept on the scalar unit (the compiler
+// otherwise folds the row's product into a 64-bit multiply-add per lane).
+__device__ inline uint64_t scalar(uint64_t v) {
+  asm("" : "+s"(v));
+  return v;
+}
+
+// One vector as it lies in memory (16 bytes, or one element), so that loads can
+// be issued apart from the conversion; zero bits are zeros in either type.
+template <typename T, int VW> struct Raw;
+template <> struct Raw<float, 4> {
+  float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  __device__ inline void ld(const float *p) { r = *reinterpret_cast<const float4 *>(p); }
+  __device__ inline void get(float (&v)[4]) const { v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w; }
+};
+template <> struct Raw<uint16_t, 8> {
+  uint4 r = make_uint4(0, 0, 0, 0);
+  __device__ inline void ld(const uint16_t *p) { r = *reinterpret_cast<const uint4 *>(p); }
+  __device__ inline void get(float (&v)[8]) const {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <typename T> struct Raw<T, 1> {
+  T r = 0;
+  __device__ inline void ld(const T *p) { r = *p; }
+  __device__ inline void get(float (&v)[1]) const { v[0] = Store<T>::ld(&r); }
+};
 
 // Edges [b, e) of row d; bounds from memory are held inside [0, E].
 __device__ inline void row_bounds(const int *ptr, int d, int E, int *b, int *e) {
@@ -195,13 +232,40 @@ __device__ inline void for_decisions(int b, int cnt, int H, const Drop &dr, F f)
   }
 }
 
+// Block b's slice (or part) of `slices`, and its number among the slice's
+// `blocks` blocks.  Consecutive blocks go to the eight XCDs in turn, so a slice
+// stays on one XCD (slices 1, 2, 4, 8 or a multiple of 8, eight at a time).
+struct Slot {
+  int slice, block;
+};
+__device__ inline Slot slot_of(int slices, int blocks) {
+  const int b = blockIdx.x;
+  if (slices <= 8) return Slot{b % slices, b / slices};
+  return Slot{((b >> 3) / blocks) * 8 + (b & 7), (b >> 3) % blocks};
+}
+
 // ------------------------------------------------------------------ products
 
-// Lane layout of a dot product over `H` heads of `P` vectors each: lane =
-// (edge sub, head, part), powers of two.
+// Lane layout of the dot products of rows [K][C] over H heads, in vectors of
+// VW elements.
+//   natural (H and the vectors of a head powers of two, a component's vectors
+//   at most a wave): lane = (edge sub, component sub, vector of the
+//   component), so that four neighbouring lanes read 64 contiguous bytes: the
+//   vector cache looks up one line for four lanes at a time, and a head's
+//   lanes side by side instead (the other layout) cost twice the lookups
+//   where a head has 32 bytes of a component;
+//   by head (any shape): lane = (edge sub, head, part).
+// The partial products of a head are summed over the lane bits [0, low) and
+// [hi0, hi1).
 struct Team {
-  int LTl, Hpl;  // log2 of parts per head, of padded heads
+  bool natural;
+  int low, hi0, hi1;
+  int esh;           // log2 of the lanes an edge takes
+  int NCl, KSl;      // natural: log2 of a component's vectors, of the components side by side
+  int rounds, nit;   // vectors a lane: rounds of nit
 };
+
+constexpr int kMaxNit = 7;  // vectors of A a lane keeps in registers
 
 inline int log2_ceil(int n) {
   int l = 0;
@@ -209,11 +273,29 @@ inline int log2_ceil(int n) {
   return l;
 }
 
-inline Team make_team(int H, int vectors) {
-  Team t;
-  t.Hpl = log2_ceil(H);
-  const int want = log2_ceil(vectors);
-  t.LTl = want < 6 - t.Hpl ? want : 6 - t.Hpl;
+inline bool pow2(int n) { return (n & (n - 1)) == 0; }
+
+inline Team make_team(int K, int H, int P) {
+  Team t{};
+  const int NC = H * P;
+  t.natural = pow2(H) && pow2(P) && NC <= kWave;
+  if (t.natural) {
+    t.NCl = log2_ceil(NC);
+    const int want = log2_ceil(K);
+    t.KSl = want < 6 - t.NCl ? want : 6 - t.NCl;
+    t.low = log2_ceil(P);
+    t.hi0 = t.NCl;
+    t.hi1 = t.esh = t.NCl + t.KSl;
+    t.nit = (K + (1 << t.KSl) - 1) >> t.KSl;
+  } else {
+    const int Hpl = log2_ceil(H), want = log2_ceil(K * P);
+    t.low = want < 6 - Hpl ? want : 6 - Hpl;
+    t.hi0 = t.hi1 = 0;
+    t.esh = t.low + Hpl;
+    t.nit = (K * P + (1 << t.low) - 1) >> t.low;
+  }
+  t.rounds = (t.nit + kMaxNit - 1) / kMaxNit;
+  t.nit = (t.nit + t.rounds - 1) / t.rounds;
   return t;
 }
 
@@ -221,102 +303,136 @@ template <int CTRL> __device__ inline float dpp_move(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
 }
 
-// dot[u] summed over teams of 2^LTl lanes; every lane of a team gets the sum.
-// Up to 16 lanes the steps are DPP moves inside a row of 16 (a quad's lanes
-// hold the same value when the mirrors swap quads), no LDS permutes.
-template <int U>
-__device__ inline void team_sum(float (&dot)[U], int LTl) {
-  if (LTl > 0)
-#pragma unroll
-    for (int u = 0; u < U; ++u) dot[u] += dpp_move<0xB1>(dot[u]);   // quad [1,0,3,2]
-  if (LTl > 1)
-#pragma unroll
-    for (int u = 0; u < U; ++u) dot[u] += dpp_move<0x4E>(dot[u]);   // quad [2,3,0,1]
-  if (LTl > 2)
-#pragma unroll
-    for (int u = 0; u < U; ++u) dot[u] += dpp_move<0x141>(dot[u]);  // mirror within 8
-  if (LTl > 3)
-#pragma unroll
-    for (int u = 0; u < U; ++u) dot[u] += dpp_move<0x140>(dot[u]);  // mirror within 16
-  if (LTl > 4)
-#pragma unroll
-    for (int u = 0; u < U; ++u) dot[u] += __shfl_xor(dot[u], 16);
-  if (LTl > 5)
-#pragma unroll
-    for (int u = 0; u < U; ++u) dot[u] += __shfl_xor(dot[u], 32);
+// v + v of the lane that differs in bit `bit` only
+__device__ inline float add_across(float v, int bit) {
+  if (bit == 5) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if (bit == 4) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return v + __shfl_xor(v, 1 << bit);
 }
 
-// lds[i * H + h] = sum over the head's vectors of A . B[scol[i]], i < cnt.
-// A stays in registers, NIT vectors a lane.  Head h's vector j lies at
-// (j / P) C + h Ch + (j % P) VW.  ONE: a wave takes one edge at a time (teams
-// fill it), so the row's address is scalar work and the loads are scalar base
-// plus the lane's fixed offset.
-template <typename TA, typename TB, int VW, int NIT, bool ONE>
-__device__ inline void edge_dots(const TA *arow, const TB *B, int64_t ldb, const int *scol, int cnt, int H, int C,
-                                 int Ch, int nvec, Team tm, float *lds) {
-  constexpr int U = NIT >= 8 ? 1 : 8 / NIT;  // eight loads in flight
-  const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x >> 6);
-  const int LT = 1 << tm.LTl;
-  const int t = lane & (LT - 1), hh = (lane >> tm.LTl) & ((1 << tm.Hpl) - 1);
-  const int es = ONE ? 0 : lane >> (tm.LTl + tm.Hpl);
-  const int EPW = ONE ? 1 : kWave >> (tm.LTl + tm.Hpl);
-  const int h = min(hh, H - 1);
-  const int P = Ch / VW;
-  for (int c0 = 0; c0 < nvec; c0 += LT * NIT) {
-    float af[NIT][VW];
-    int off[NIT];
-    bool ok[NIT];
+// dot[u] summed over the team; every lane of a team gets the sum.  The low
+// bits take DPP moves inside a row of 16 (a quad's lanes hold the same value
+// when the mirrors swap quads).
+template <int U>
+__device__ inline void team_sum(float (&dot)[U], const Team &tm) {
+  if (tm.low > 0)
 #pragma unroll
-    for (int i = 0; i < NIT; ++i) {
-      const int j = c0 + i * LT + t;
-      ok[i] = j < nvec;
-      const int jj = ok[i] ? j : nvec - 1;
-      off[i] = (jj / P) * C + h * Ch + (jj % P) * VW;
-      Vec<TA, VW>::ld(arow + off[i], af[i]);
+    for (int u = 0; u < U; ++u) dot[u] += dpp_move<0xB1>(dot[u]);   // quad [1,0,3,2]
+  if (tm.low > 1)
+#pragma unroll
+    for (int u = 0; u < U; ++u) dot[u] += dpp_move<0x4E>(dot[u]);   // quad [2,3,0,1]
+  if (tm.low > 2)
+#pragma unroll
+    for (int u = 0; u < U; ++u) dot[u] += dpp_move<0x141>(dot[u]);  // mirror within 8
+  if (tm.low > 3)
+#pragma unroll
+    for (int u = 0; u < U; ++u) dot[u] += dpp_move<0x140>(dot[u]);  // mirror within 16
+  for (int bit = 4; bit < tm.low; ++bit)
+#pragma unroll
+    for (int u = 0; u < U; ++u) dot[u] = add_across(dot[u], bit);
+  for (int bit = tm.hi0; bit < tm.hi1; ++bit)
+#pragma unroll
+    for (int u = 0; u < U; ++u) dot[u] = add_across(dot[u], bit);
+}
+
+// put(i, h, dot, first) for edges i = i_first + es + EPW-wide steps of
+// `stride` below cnt, dot = sum over the head's vectors of A . B[scol[i]] (row
+// 0 for a source of -1).  A stays in registers, NIT vectors a lane; what does
+// not fit is added by further rounds (first = false).  ONE: a wave takes one
+// edge at a time, so the row's address is scalar work.
+template <typename TA, typename TB, int VW, int NIT, bool ONE, typename Put>
+__device__ inline void edge_dots(const TA *arow, const TB *B, int64_t ldb, const int *scol, int i_first, int stride,
+                                 int cnt, int K, int H, int C, const Team &tm, Put put) {
+  constexpr int U = NIT == 1 ? 8 : NIT == 2 ? 4 : NIT == 3 ? 3 : 2;  // 6 to 14 loads in flight
+  const int lane = threadIdx.x & (kWave - 1);
+  const int Ch = C / H, P = Ch / VW;
+  const int es = ONE ? 0 : lane >> tm.esh;
+  const uint32_t pitch = static_cast<uint32_t>(ldb * sizeof(TB));
+  // this lane's head, first vector and step: vector n of the lane lies at
+  // component k(n), and exists while k(n) < K
+  int h, t0;
+  if (tm.natural) {
+    const int col = lane & ((1 << tm.NCl) - 1);
+    h = col >> tm.low;
+    t0 = (lane >> tm.NCl) & ((1 << tm.KSl) - 1);
+  } else {
+    h = (lane >> tm.low) & ((1 << (tm.esh - tm.low)) - 1);
+    t0 = lane & ((1 << tm.low) - 1);
+  }
+  const bool writes = (lane & ((1 << tm.low) - 1)) == 0 && (!tm.natural || t0 == 0) && h < H;
+  const int hc = min(h, H - 1);
+  // vector m of the lane goes to round m % rounds, so that only a round's last
+  // (n = NIT - 1) may be missing in some or all lanes
+  for (int r = 0; r < tm.rounds; ++r) {
+    float af[NIT][VW];
+    uint32_t off[NIT];
+    bool have = true;
+#pragma unroll
+    for (int n = 0; n < NIT; ++n) {
+      const int m = n * tm.rounds + r;
+      if (tm.natural) {
+        const int k = (m << tm.KSl) + t0;
+        have = k < K;
+        off[n] = min(k, K - 1) * C + (lane & ((1 << tm.NCl) - 1)) * VW;
+      } else {
+        const int j = (m << tm.low) + t0;
+        have = j < K * P;
+        const int jj = min(j, K * P - 1);
+        off[n] = (jj / P) * C + hc * Ch + (jj % P) * VW;
+      }
+      Vec<TA, VW>::ld(arow + off[n], af[n]);
+      off[n] *= sizeof(TB);
     }
-    for (int i0 = wave * EPW; i0 < cnt; i0 += kWaves * EPW * U) {
-      float v[U][NIT][VW], dot[U];
+#pragma unroll
+    for (int x = 0; x < VW; ++x) af[NIT - 1][x] = have ? af[NIT - 1][x] : 0.0f;
+    for (int i0 = i_first; i0 < cnt; i0 += stride * U) {
+      Raw<TB, VW> v[U][NIT];
+      float dot[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = min(i0 + u * kWaves * EPW + es, cnt - 1);
-        const int s = ONE ? uniform(scol[i]) : scol[i];
-        const TB *row = B + static_cast<int64_t>(s) * ldb;
+        const int i = min(i0 + u * stride + es, cnt - 1);
+        const uint32_t s = max(ONE ? uniform(scol[i]) : scol[i], 0);
+        uint64_t at = static_cast<uint64_t>(s) * pitch;
+        if constexpr (ONE) at = scalar(at);
+        const char *row = reinterpret_cast<const char *>(B) + at;
 #pragma unroll
-        for (int n = 0; n < NIT; ++n) Vec<TB, VW>::ld(row + off[n], v[u][n]);
+        for (int n = 0; n < NIT - 1; ++n) v[u][n].ld(reinterpret_cast<const TB *>(row + off[n]));
+        // a vector that is not there is not read: what lies at a clamped place
+        // (an infinity) must not meet the 0 in A, nor cost a lookup
+        if (have) v[u][NIT - 1].ld(reinterpret_cast<const TB *>(row + off[NIT - 1]));
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         dot[u] = 0.0f;
 #pragma unroll
         for (int n = 0; n < NIT; ++n) {
-          float part = 0.0f;
+          float x[VW];
+          v[u][n].get(x);
 #pragma unroll
-          for (int x = 0; x < VW; ++x) part += af[n][x] * v[u][n][x];
-          dot[u] += ok[n] ? part : 0.0f;
+          for (int y = 0; y < VW; ++y) dot[u] = fmaf(af[n][y], x[y], dot[u]);
         }
       }
-      team_sum<U>(dot, tm.LTl);
+      team_sum<U>(dot, tm);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * kWaves * EPW + es;
-        if (t == 0 && hh < H && i < cnt) lds[i * H + hh] = c0 == 0 ? dot[u] : lds[i * H + hh] + dot[u];
+        const int i = i0 + u * stride + es;
+        if (writes && i < cnt) put(i, h, dot[u], r == 0);
       }
     }
   }
 }
 
-// The source of each of cnt edges, sources outside the list as row 0 (their
-// logits are masked).
-__device__ inline void stage_sources(const int *src, int b, int cnt, int n_src, int *scol) {
-  for (int i = threadIdx.x; i < cnt; i += kThreads) {
-    const int s = src[b + i];
-    scol[i] = static_cast<unsigned>(s) < static_cast<unsigned>(n_src) ? s : 0;
-  }
-}
-
 struct LogitArgs {
   const int *row_ptr, *src;
-  int n_dst, n_src, E, T, H, D;   // H heads of two maps
+  int n_dst, n_src, E, H, D;      // H heads of two maps
+  int T, TP;                      // edges in LDS at a time; of a piece (longer rows are cut)
+  int Hpl;                        // log2 of the maps' columns, padded
   int64_t ldq, ldk;
   float scale;
   const float *bias;              // [E][2H] or null
@@ -324,19 +440,29 @@ struct LogitArgs {
   const float *lam;
   Drop drop;
   Team team;
-  float *logits;                  // [E][2H] or null (no backward and no long row)
-  float *w;                       // [E][H]
+  float *logits;                  // [E][2H] or null (no backward, and no row beyond T)
+  float *w;                       // [H][ldw]
+  int64_t ldw;
   float2 *stats;                  // [n_dst][2H]
   int *dst;                       // [E]
   float2 *piece_stats;            // [pieces][2H]
 };
 
-// One block per row (or piece): logits, softmax statistics and, for whole
-// rows, the edge weights.
+// Edge weights of [b, b + cnt) from their logits (in LDS or memory).
+__device__ inline void edge_weights(const LogitArgs &a, const float2 *lg, const float2 *fin, int b, int cnt) {
+  for_decisions(b, cnt, a.H, a.drop, [&](int at, int i, int h, float m) {
+    const float2 l = lg[at];
+    const float a0 = weight_of(l.x, fin[2 * h]), a1 = weight_of(l.y, fin[2 * h + 1]);
+    a.w[h * a.ldw + b + i] = m == 0.0f ? 0.0f : m * (a0 - a.lam[h] * a1);
+  });
+}
+
+// One block per row (or piece): logits, T edges at a time, with the running
+// maximum and sum of each map, and, for whole rows, the edge weights.
 template <typename T, int VW, int NIT, bool ONE>
 __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *__restrict__ q,
                                                           const T *__restrict__ k) {
-  extern __shared__ float lg[];  // [T][2H], then the sources [T]
+  extern __shared__ __align__(16) float lg[];  // [T][2H], then the sources [T]
   int *scol = reinterpret_cast<int *>(lg + a.T * 2 * a.H);
   __shared__ float red[kWaves][kWave];
   __shared__ float2 fin[kWave];
@@ -346,45 +472,57 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *
   if (p < 0) {
     d = blockIdx.x;
     row_bounds(a.row_ptr, d, a.E, &b, &e);
-    if (e - b > a.T || e == b) return;
+    if (e - b > a.TP || e == b) return;
   } else {
-    const Piece pc = find_piece(p, a.T, a.row_ptr, a.n_dst, a.E,
+    const Piece pc = find_piece(p, a.TP, a.row_ptr, a.n_dst, a.E,
                                 [&](int pos) { return row_by_search(a.row_ptr, a.n_dst, pos); });
     if (pc.row < 0) return;
     d = pc.row;
     b = pc.begin;
     e = pc.end;
   }
-  const int cnt = e - b;
-  for (int i = threadIdx.x; i < cnt; i += kThreads) a.dst[b + i] = d;
-  stage_sources(a.src, b, cnt, a.n_src, scol);
-  __syncthreads();
-  edge_dots<T, T, VW, NIT, ONE>(q + static_cast<int64_t>(d) * a.ldq, k, a.ldk, scol, cnt, H2, H2 * a.D, a.D, a.D / VW,
-                                a.team, lg);
-  __syncthreads();
-  const int Hp = 1 << a.team.Hpl;
-  const int col = threadIdx.x & (Hp - 1), r0 = threadIdx.x >> a.team.Hpl, R = kThreads >> a.team.Hpl;
-  float M = -INFINITY;
-  if (col < H2) {
-    for (int i = r0; i < cnt; i += R) {
-      const int64_t o = static_cast<int64_t>(b + i) * H2 + col;
-      float l = lg[i * H2 + col] * a.scale;
-      if (a.bias) {
-        const float bv = a.bias[o];
-        l = bv == -INFINITY ? -INFINITY : l + bv;  // a bias of -inf masks, whatever the product is
-      }
-      if ((a.mask && a.mask[b + i] == 0) || static_cast<unsigned>(a.src[b + i]) >= static_cast<unsigned>(a.n_src))
-        l = -INFINITY;
-      lg[i * H2 + col] = l;
-      if (a.logits) a.logits[o] = l;
-      M = fmaxf(M, l);
+  const int Hp = 1 << a.Hpl;
+  const int col = threadIdx.x & (Hp - 1), r0 = threadIdx.x >> a.Hpl, R = kThreads >> a.Hpl;
+  float M = -INFINITY, S = 0.0f;
+  for (int c0 = b; c0 < e; c0 += a.T) {
+    const int cnt = min(a.T, e - c0);
+    __syncthreads();  // the last chunk's logits are no longer read
+    for (int i = threadIdx.x; i < cnt; i += kThreads) {
+      const int s = a.src[c0 + i];
+      // -1: takes no part; its products are taken with row 0 and not used
+      const bool live = static_cast<unsigned>(s) < static_cast<unsigned>(a.n_src) && !(a.mask && a.mask[c0 + i] == 0);
+      scol[i] = live ? s : -1;
+      a.dst[c0 + i] = d;
     }
+    __syncthreads();
+    const int step = ONE ? 1 : kWave >> a.team.esh;
+    edge_dots<T, T, VW, NIT, ONE>(q + static_cast<int64_t>(d) * a.ldq, k, a.ldk, scol,
+                                  uniform(threadIdx.x >> 6) * step, kWaves * step, cnt, 1, H2, H2 * a.D, a.team,
+                                  [&](int i, int h, float x, bool first) {
+                                    lg[i * H2 + h] = first ? x : lg[i * H2 + h] + x;
+                                  });
+    __syncthreads();
+    float Mc = -INFINITY;
+    if (col < H2)
+      for (int i = r0; i < cnt; i += R) {
+        const int64_t o = static_cast<int64_t>(c0 + i) * H2 + col;
+        float l = lg[i * H2 + col] * a.scale;
+        if (a.bias) {
+          const float bv = a.bias[o];
+          l = bv == -INFINITY ? -INFINITY : l + bv;  // a bias of -inf masks, whatever the product is
+        }
+        if (scol[i] < 0) l = -INFINITY;
+        lg[i * H2 + col] = l;
+        if (a.logits) a.logits[o] = l;
+        Mc = fmaxf(Mc, l);
+      }
+    const float Mn = fmaxf(M, column_reduce(Mc, Hp, red, MaxOp()));
+    float Sc = 0.0f;
+    if (col < H2 && Mn != -INFINITY)
+      for (int i = r0; i < cnt; i += R) Sc += __expf(lg[i * H2 + col] - Mn);
+    S = (M == -INFINITY ? 0.0f : S * __expf(M - Mn)) + column_reduce(Sc, Hp, red, SumOp());
+    M = Mn;
   }
-  M = column_reduce(M, Hp, red, MaxOp());
-  float S = 0.0f;
-  if (col < H2 && M != -INFINITY)
-    for (int i = r0; i < cnt; i += R) S += __expf(lg[i * H2 + col] - M);
-  S = column_reduce(S, Hp, red, SumOp());
   if (p >= 0) {
     if (r0 == 0 && col < H2) a.piece_stats[static_cast<int64_t>(p) * H2 + col] = make_float2(M, S);
     return;
@@ -395,32 +533,32 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *
     a.stats[static_cast<int64_t>(d) * H2 + col] = st;
   }
   __syncthreads();
-  for_decisions(b, cnt, a.H, a.drop, [&](int at, int, int h, float m) {
-    const float a0 = weight_of(lg[2 * at], fin[2 * h]), a1 = weight_of(lg[2 * at + 1], fin[2 * h + 1]);
-    a.w[static_cast<int64_t>(b) * a.H + at] = m == 0.0f ? 0.0f : m * (a0 - a.lam[h] * a1);
-  });
+  if (e - b <= a.T)
+    edge_weights(a, reinterpret_cast<const float2 *>(lg), fin, b, e - b);
+  else  // written by this block, so its own barrier and cache order them
+    edge_weights(a, reinterpret_cast<const float2 *>(a.logits) + static_cast<int64_t>(b) * a.H, fin, b, e - b);
 }
 
 // Long rows: the pieces' statistics joined, then their edge weights.
 __global__ void __launch_bounds__(kThreads) long_weights_kernel(LogitArgs a) {
   __shared__ float red[kWaves][kWave];
   __shared__ float2 fin[kWave];
-  const Piece pc = find_piece(blockIdx.x, a.T, a.row_ptr, a.n_dst, a.E, [&](int pos) { return a.dst[pos]; });
+  const Piece pc = find_piece(blockIdx.x, a.TP, a.row_ptr, a.n_dst, a.E, [&](int pos) { return a.dst[pos]; });
   if (pc.row < 0) return;
   int b, e;
   row_bounds(a.row_ptr, pc.row, a.E, &b, &e);
-  const int H2 = 2 * a.H, Hp = 1 << a.team.Hpl;
-  const int col = threadIdx.x & (Hp - 1), r0 = threadIdx.x >> a.team.Hpl, R = kThreads >> a.team.Hpl;
-  const int n = piece_count(b, e, a.T);
+  const int H2 = 2 * a.H, Hp = 1 << a.Hpl;
+  const int col = threadIdx.x & (Hp - 1), r0 = threadIdx.x >> a.Hpl, R = kThreads >> a.Hpl;
+  const int n = piece_count(b, e, a.TP);
   float M = -INFINITY;
   if (col < H2)
     for (int i = r0; i < n; i += R)
-      M = fmaxf(M, a.piece_stats[static_cast<int64_t>(piece_id(b, a.T, i)) * H2 + col].x);
+      M = fmaxf(M, a.piece_stats[static_cast<int64_t>(piece_id(b, a.TP, i)) * H2 + col].x);
   M = column_reduce(M, Hp, red, MaxOp());
   float S = 0.0f;
   if (col < H2 && M != -INFINITY)
     for (int i = r0; i < n; i += R) {
-      const float2 st = a.piece_stats[static_cast<int64_t>(piece_id(b, a.T, i)) * H2 + col];
+      const float2 st = a.piece_stats[static_cast<int64_t>(piece_id(b, a.TP, i)) * H2 + col];
       if (st.x != -INFINITY) S += st.y * __expf(st.x - M);
     }
   S = column_reduce(S, Hp, red, SumOp());
@@ -429,43 +567,96 @@ __global__ void __launch_bounds__(kThreads) long_weights_kernel(LogitArgs a) {
     if (pc.begin == b) a.stats[static_cast<int64_t>(pc.row) * H2 + col] = fin[col];
   }
   __syncthreads();
-  const float2 *lg = reinterpret_cast<const float2 *>(a.logits) + static_cast<int64_t>(pc.begin) * a.H;
-  for_decisions(pc.begin, pc.end - pc.begin, a.H, a.drop, [&](int at, int, int h, float m) {
-    const float2 l = lg[at];
-    const float a0 = weight_of(l.x, fin[2 * h]), a1 = weight_of(l.y, fin[2 * h + 1]);
-    a.w[static_cast<int64_t>(pc.begin) * a.H + at] = m == 0.0f ? 0.0f : m * (a0 - a.lam[h] * a1);
-  });
+  edge_weights(a, reinterpret_cast<const float2 *>(a.logits) + static_cast<int64_t>(pc.begin) * a.H, fin, pc.begin,
+               pc.end - pc.begin);
+}
+
+struct DotArgs {
+  const int *row_ptr, *src, *dst;
+  int n_dst, n_src, E, T;
+  int K, C, H;
+  int64_t ldv;
+  Team team;
+  int parts, unit0, units, blocks;
+  float *u;  // [E][H]
+};
+
+// u[e][h] = <grad_out[d], v[src]> over the head's channels.  One wave per (row
+// or piece, part of its edges).  Part p of every row goes to XCD p % 8: rows
+// list their sources in ascending order, so a part meets about the same
+// stretch of v in every row, and the XCD's L2 holds it.
+template <typename T, int VW, int NIT, bool ONE>
+__global__ void __launch_bounds__(kThreads) value_dots_kernel(DotArgs a, const float *__restrict__ go,
+                                                              const T *__restrict__ v) {
+  __shared__ int scol[kWaves][kWave];
+  const Slot sl = slot_of(a.parts, a.blocks);
+  const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x >> 6);
+  const int unit = a.unit0 + sl.block * kWaves + wave;
+  if (unit >= a.units) return;
+  int d = unit, b, e;
+  if (unit < a.n_dst) {
+    row_bounds(a.row_ptr, d, a.E, &b, &e);
+    if (e - b > a.T) return;
+  } else {
+    const Piece pc = find_piece(unit - a.n_dst, a.T, a.row_ptr, a.n_dst, a.E, [&](int pos) { return a.dst[pos]; });
+    if (pc.row < 0) return;
+    d = pc.row;
+    b = pc.begin;
+    e = pc.end;
+  }
+  const int64_t len = e - b;
+  e = uniform(b + static_cast<int>(len * (sl.slice + 1) / a.parts));
+  b = uniform(b + static_cast<int>(len * sl.slice / a.parts));
+  for (int c0 = b; c0 < e; c0 += kWave) {
+    const int cnt = min(kWave, e - c0);
+    const int s = lane < cnt ? a.src[c0 + lane] : -1;
+    scol[wave][lane] = static_cast<unsigned>(s) < static_cast<unsigned>(a.n_src) ? s : -1;
+    wave_lds_order();
+    edge_dots<float, T, VW, NIT, ONE>(go + static_cast<int64_t>(d) * a.K * a.C, v, a.ldv, scol[wave], 0,
+                                      ONE ? 1 : kWave >> a.team.esh, cnt, a.K, a.H, a.C, a.team,
+                                      [&](int i, int h, float x, bool first) {
+                                        float *o = a.u + static_cast<int64_t>(c0 + i) * a.H + h;
+                                        *o = first ? x : *o + x;
+                                      });
+    wave_lds_order();
+  }
 }
 
 struct GradArgs {
-  const int *row_ptr, *src, *dst;
-  int n_dst, n_src, E, T, H, C, K;
-  int64_t ldv;
+  const int *row_ptr, *dst;
+  int n_dst, E, H;
+  int T, TP, Hpl;
   const float *lam;
   Drop drop;
-  Team team;
   const float2 *logits;  // [E][H] pairs of maps
   const float2 *stats;   // [n_dst][H] pairs of (M, 1/S): two entries a head
   float2 *dl;            // [E][H] pairs: gradient of the logits before the scale
+  float *dlp;            // the same as planes [2H][ldw]
+  int64_t ldw;
+  float *wr;             // [E][H] the forward's weights, again
   float *t1;             // [n_dst][H] sum_e a1 u
-  float *u;              // [E][H] m <grad_out, v> of long rows, or null
+  float *u;              // [E][H] in: <grad_out, v>; where a row does not stay in LDS, m times that
   float2 *piece_t;       // [pieces][H] (sum a0 u, sum a1 u)
 };
 
-__device__ inline void logit_grads(const GradArgs &a, int64_t o, int h, float u, float2 t, const float4 *st) {
-  const float2 l = a.logits[o];
-  const float a0 = weight_of(l.x, make_float2(st[h].x, st[h].y)), a1 = weight_of(l.y, make_float2(st[h].z, st[h].w));
-  // a weight of exactly 0 (masked) has no gradient, whatever the row of v holds
-  a.dl[o] = make_float2(a0 == 0.0f ? 0.0f : a0 * (u - t.x), a1 == 0.0f ? 0.0f : -a.lam[h] * a1 * (u - t.y));
+__device__ inline float2 weights_of(float2 l, const float4 st) {
+  return make_float2(weight_of(l.x, make_float2(st.x, st.y)), weight_of(l.y, make_float2(st.z, st.w)));
 }
 
-// One block per row (or piece): u = m <grad_out, v> per edge and head, then the
-// softmax's backward for both maps.
-template <typename T, int VW, int NIT, bool ONE>
-__global__ void __launch_bounds__(kThreads) logit_grad_kernel(GradArgs a, const float *__restrict__ go,
-                                                              const T *__restrict__ v) {
-  extern __shared__ float us[];  // [T][H], then the sources [T]
-  int *scol = reinterpret_cast<int *>(us + a.T * a.H);
+__device__ inline void logit_grads(const GradArgs &a, int64_t e, int h, float u, float2 t, const float4 *st) {
+  const float2 w = weights_of(a.logits[e * a.H + h], st[h]);
+  // a weight of exactly 0 (masked) has no gradient, whatever the row of v holds
+  const float2 g =
+      make_float2(w.x == 0.0f ? 0.0f : w.x * (u - t.x), w.y == 0.0f ? 0.0f : -a.lam[h] * w.y * (u - t.y));
+  a.dl[e * a.H + h] = g;
+  a.dlp[2 * h * a.ldw + e] = g.x;
+  a.dlp[(2 * h + 1) * a.ldw + e] = g.y;
+}
+
+// One block per row (or piece): the softmax's backward for both maps, T edges
+// at a time.
+__global__ void __launch_bounds__(kThreads) logit_grad_kernel(GradArgs a) {
+  extern __shared__ float us[];  // [T][H]
   __shared__ float red[kWaves][kWave];
   __shared__ float4 st[kMaxHeads];
   __shared__ float2 tt[kMaxHeads];
@@ -474,45 +665,44 @@ __global__ void __launch_bounds__(kThreads) logit_grad_kernel(GradArgs a, const 
   if (p < 0) {
     d = blockIdx.x;
     row_bounds(a.row_ptr, d, a.E, &b, &e);
-    if (e - b > a.T) return;
+    if (e - b > a.TP) return;
     if (e == b) {
       if (threadIdx.x < static_cast<unsigned>(a.H)) a.t1[static_cast<int64_t>(d) * a.H + threadIdx.x] = 0.0f;
       return;
     }
   } else {
-    const Piece pc = find_piece(p, a.T, a.row_ptr, a.n_dst, a.E, [&](int pos) { return a.dst[pos]; });
+    const Piece pc = find_piece(p, a.TP, a.row_ptr, a.n_dst, a.E, [&](int pos) { return a.dst[pos]; });
     if (pc.row < 0) return;
     d = pc.row;
     b = pc.begin;
     e = pc.end;
   }
-  const int cnt = e - b, H = a.H;
+  const int H = a.H, Hp = 1 << a.Hpl;
+  const int h = threadIdx.x & (Hp - 1), r0 = threadIdx.x >> a.Hpl, R = kThreads >> a.Hpl;
   if (threadIdx.x < static_cast<unsigned>(H))
     st[threadIdx.x] = reinterpret_cast<const float4 *>(a.stats)[static_cast<int64_t>(d) * H + threadIdx.x];
-  const int Ch = a.C / H;
-  stage_sources(a.src, b, cnt, a.n_src, scol);
-  __syncthreads();
-  edge_dots<float, T, VW, NIT, ONE>(go + static_cast<int64_t>(d) * a.K * a.C, v, a.ldv, scol, cnt, H, a.C, Ch,
-                                    a.K * (Ch / VW), a.team, us);
-  __syncthreads();
-  for_decisions(b, cnt, H, a.drop, [&](int at, int, int, float m) {
-    const float x = m == 0.0f ? 0.0f : m * us[at];
-    us[at] = x;
-    if (p >= 0) a.u[static_cast<int64_t>(b) * H + at] = x;
-  });
-  __syncthreads();
-  const int Hp = 1 << a.team.Hpl;
-  const int h = threadIdx.x & (Hp - 1), r0 = threadIdx.x >> a.team.Hpl, R = kThreads >> a.team.Hpl;
+  const bool keep = p >= 0 || e - b > a.T;  // u does not stay in LDS until the row's sums are known
   float t0 = 0.0f, t1 = 0.0f;
-  if (h < H)
-    for (int i = r0; i < cnt; i += R) {
-      const float2 l = a.logits[static_cast<int64_t>(b + i) * H + h];
-      const float a0 = weight_of(l.x, make_float2(st[h].x, st[h].y));
-      const float a1 = weight_of(l.y, make_float2(st[h].z, st[h].w));
-      const float x = us[i * H + h];
-      t0 += a0 == 0.0f ? 0.0f : a0 * x;
-      t1 += a1 == 0.0f ? 0.0f : a1 * x;
-    }
+  for (int c0 = b; c0 < e; c0 += a.T) {
+    const int cnt = min(a.T, e - c0);
+    const int64_t o0 = static_cast<int64_t>(c0) * H;
+    __syncthreads();
+    for_decisions(c0, cnt, H, a.drop, [&](int at, int, int hd, float m) {
+      const float2 w = weights_of(a.logits[o0 + at], st[hd]);
+      a.wr[o0 + at] = m == 0.0f ? 0.0f : m * (w.x - a.lam[hd] * w.y);
+      const float x = m == 0.0f ? 0.0f : m * a.u[o0 + at];
+      us[at] = x;
+      if (keep) a.u[o0 + at] = x;
+    });
+    __syncthreads();
+    if (h < H)
+      for (int i = r0; i < cnt; i += R) {
+        const float2 w = weights_of(a.logits[o0 + i * H + h], st[h]);
+        const float x = us[i * H + h];
+        t0 += w.x == 0.0f ? 0.0f : w.x * x;
+        t1 += w.y == 0.0f ? 0.0f : w.y * x;
+      }
+  }
   t0 = column_reduce(t0, Hp, red, SumOp());
   t1 = column_reduce(t1, Hp, red, SumOp());
   if (p >= 0) {
@@ -525,8 +715,8 @@ __global__ void __launch_bounds__(kThreads) logit_grad_kernel(GradArgs a, const 
   }
   __syncthreads();
   if (h < H)
-    for (int i = r0; i < cnt; i += R)
-      logit_grads(a, static_cast<int64_t>(b + i) * H + h, h, us[i * H + h], tt[h], st);
+    for (int i = b + r0; i < e; i += R)
+      logit_grads(a, i, h, keep ? a.u[static_cast<int64_t>(i) * H + h] : us[(i - b) * H + h], tt[h], st);
 }
 
 // Long rows: the pieces' sums joined, then the logits' gradients.
@@ -534,19 +724,19 @@ __global__ void __launch_bounds__(kThreads) long_grad_kernel(GradArgs a) {
   __shared__ float red[kWaves][kWave];
   __shared__ float4 st[kMaxHeads];
   __shared__ float2 tt[kMaxHeads];
-  const Piece pc = find_piece(blockIdx.x, a.T, a.row_ptr, a.n_dst, a.E, [&](int pos) { return a.dst[pos]; });
+  const Piece pc = find_piece(blockIdx.x, a.TP, a.row_ptr, a.n_dst, a.E, [&](int pos) { return a.dst[pos]; });
   if (pc.row < 0) return;
   int b, e;
   row_bounds(a.row_ptr, pc.row, a.E, &b, &e);
-  const int H = a.H, Hp = 1 << a.team.Hpl;
-  const int h = threadIdx.x & (Hp - 1), r0 = threadIdx.x >> a.team.Hpl, R = kThreads >> a.team.Hpl;
+  const int H = a.H, Hp = 1 << a.Hpl;
+  const int h = threadIdx.x & (Hp - 1), r0 = threadIdx.x >> a.Hpl, R = kThreads >> a.Hpl;
   if (threadIdx.x < static_cast<unsigned>(H))
     st[threadIdx.x] = reinterpret_cast<const float4 *>(a.stats)[static_cast<int64_t>(pc.row) * H + threadIdx.x];
-  const int n = piece_count(b, e, a.T);
+  const int n = piece_count(b, e, a.TP);
   float t0 = 0.0f, t1 = 0.0f;
   if (h < H)
     for (int i = r0; i < n; i += R) {
-      const float2 t = a.piece_t[static_cast<int64_t>(piece_id(b, a.T, i)) * H + h];
+      const float2 t = a.piece_t[static_cast<int64_t>(piece_id(b, a.TP, i)) * H + h];
       t0 += t.x;
       t1 += t.y;
     }
@@ -558,10 +748,8 @@ __global__ void __launch_bounds__(kThreads) long_grad_kernel(GradArgs a) {
   }
   __syncthreads();
   if (h < H)
-    for (int i = pc.begin + r0; i < pc.end; i += R) {
-      const int64_t o = static_cast<int64_t>(i) * H + h;
-      logit_grads(a, o, h, a.u[o], tt[h], st);
-    }
+    for (int i = pc.begin + r0; i < pc.end; i += R)
+      logit_grads(a, i, h, a.u[static_cast<int64_t>(i) * H + h], tt[h], st);
 }
 
 // grad_lam[h] = -sum_d t1[d][h], one block a head, in a fixed order
@@ -581,120 +769,159 @@ __global__ void __launch_bounds__(kThreads) lam_grad_kernel(const float *__restr
 
 // ---------------------------------------------------------------------- sums
 
+// Edges in the order of their sources: the row each came to and its weights
+// and logit gradients as planes, so that every slice of the sums below reads
+// them in sequence.  One wave per 64 edges; a lane reads its edge's rows.
+template <bool V4>
+__global__ void __launch_bounds__(kThreads) regroup_kernel(const int *__restrict__ perm, const int *__restrict__ src_ptr,
+                                                           int n_src, int E, int H, const int *__restrict__ dst,
+                                                           const float *__restrict__ wr, const float *__restrict__ dl,
+                                                           int64_t ldw, int *__restrict__ dst_out,
+                                                           float *__restrict__ w_out, float *__restrict__ dl_out) {
+  const int j = blockIdx.x * kThreads + threadIdx.x;
+  if (j >= min(max(src_ptr[n_src], 0), E)) return;
+  const int e = perm[j];
+  const bool live = static_cast<unsigned>(e) < static_cast<unsigned>(E);
+  dst_out[j] = live ? dst[e] : -1;
+  const int64_t at = static_cast<int64_t>(live ? e : 0) * H;
+  if constexpr (V4) {
+    for (int h = 0; h < H; h += 4) {
+      const float4 x = *reinterpret_cast<const float4 *>(wr + at + h);
+      const float4 y = *reinterpret_cast<const float4 *>(dl + 2 * (at + h));
+      const float4 z = *reinterpret_cast<const float4 *>(dl + 2 * (at + h) + 4);
+      const float w[4] = {x.x, x.y, x.z, x.w}, g[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w_out[(h + k) * ldw + j] = live ? w[k] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) dl_out[(2 * h + k) * ldw + j] = live ? g[k] : 0.0f;
+    }
+  } else {
+    for (int h = 0; h < H; ++h) w_out[h * ldw + j] = live ? wr[at + h] : 0.0f;
+    for (int h = 0; h < 2 * H; ++h) dl_out[h * ldw + j] = live ? dl[2 * at + h] : 0.0f;
+  }
+}
+
 struct SumArgs {
   const int *ptr;       // [n_rows + 1]
-  const int *perm;      // edge ids in row order (PERM)
-  const int *col;       // [E] row of X of an edge
-  const int *row_of;    // [E] row of an edge
+  const int *col;       // [E] row of X of an edge, in row order
+  const int *row_of;    // [E] row of an edge; of edge perm[j] at position j where perm is given
+  const int *perm;
   int n_rows, n_x, E, T;
   int64_t ldx;
-  const float *w;       // [E][H]
+  const float *w;       // planes [H][ldw], in row order
+  int64_t ldw;
   int H, C, Ch, width;  // out row = width elements; column c of width has head (c % C) / Ch
-  int S, SV, Gl;        // slices, vectors a slice, log2 of lanes an edge
-  int BE;               // edges staged at a time
+  int S, SV, EPW;       // slices, vectors a slice, edges a wave takes at once
+  int BE;               // edges staged at a time, a multiple of what a wave takes in flight
   int unit0, units, blocks;  // first unit of the launch; rows + pieces; blocks a slice in the launch
   float scale;
   float *part;          // [pieces][width]
 };
 
-constexpr int kStage = 1024;  // weights a wave stages at a time (4 KB)
-
-template <bool PERM> __device__ inline int owner(const SumArgs &a, int pos) {
-  if constexpr (PERM) {
-    const int ed = a.perm[pos];
-    return static_cast<unsigned>(ed) < static_cast<unsigned>(a.E) ? a.row_of[ed] : -1;
-  }
-  return a.row_of[pos];
+__device__ inline int owner(const SumArgs &a, int pos) {
+  if (!a.perm) return a.row_of[pos];
+  const int ed = a.perm[pos];
+  return static_cast<unsigned>(ed) < static_cast<unsigned>(a.E) ? a.row_of[ed] : -1;
 }
 
-// The next BE edges of a list: lane i < BE holds edge j0 + i's row of X, and
-// the lanes together the BE x H weights, four a register where H allows.
-// Edges past the end and rows outside X have weight 0 and row 0.
-template <bool PERM, bool W4> struct Batch {
+// A wave stages BE edges: each head's weights side by side (SW apart), so that
+// a lane reads four edges' weights at once, and the edges' rows of X.  NR
+// registers a lane hold the next edges' weights on their way: 64 edges of up
+// to NR heads, or 16 edges of up to 4 NR.
+template <int NR> struct Batch {
   int x;
-  float4 w4[kStage / 4 / kWave];
-  float w1[kStage / kWave];
+  float w[NR];
 
-  __device__ inline void fetch(const SumArgs &a, int j0, int e, int lane) {
-    int ed = -1;
-    x = 0;
-    if (lane < a.BE && j0 + lane < e) {
-      ed = PERM ? a.perm[j0 + lane] : j0 + lane;
-      if (PERM && static_cast<unsigned>(ed) >= static_cast<unsigned>(a.E)) ed = -1;
-      if (ed >= 0) {
-        const int s = a.col[ed];
-        if (static_cast<unsigned>(s) < static_cast<unsigned>(a.n_x)) x = s;
-        else ed = -1;
-      }
-    }
-    const int per = W4 ? a.H / 4 : a.H, n = a.BE * per;
+  // Edges past the end and rows outside X have weight 0 and row 0.
+  __device__ inline void fetch(const SumArgs &a, int SWl, int j0, int e, int lane) {
+    x = -1;
+    if (lane < a.BE && j0 + lane < e) x = a.col[j0 + lane];
+    const bool live = static_cast<unsigned>(x) < static_cast<unsigned>(a.n_x);
+    const uint64_t there = __ballot(live);
+    x = live ? x : 0;
 #pragma unroll
-    for (int t = 0; t < (W4 ? kStage / 4 / kWave : kStage / kWave); ++t) {
-      const int f = t * kWave + lane;
-      if (t * kWave >= n) break;
-      const int i = f / per;
-      const int from = __shfl(ed, i & (kWave - 1));
-      const bool live = f < n && from >= 0;
-      const int64_t at = static_cast<int64_t>(from) * a.H + (f - i * per) * (W4 ? 4 : 1);
-      if constexpr (W4)
-        w4[t] = live ? *reinterpret_cast<const float4 *>(a.w + at) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      else
-        w1[t] = live ? a.w[at] : 0.0f;
+    for (int t = 0; t < NR; ++t) {
+      const int f = t * kWave + lane, h = f >> SWl, i = f & ((1 << SWl) - 1);
+      w[t] = h < a.H && ((there >> i) & 1) ? a.w[h * a.ldw + j0 + i] : 0.0f;
     }
   }
 
-  __device__ inline void stage(const SumArgs &a, int lane, float *sw, int *sx) const {
-    const int n = a.BE * (W4 ? a.H / 4 : a.H);
+  __device__ inline void stage(const SumArgs &a, int SWl, int lane, float *sw) const {
+    const int pitch = (1 << SWl) + 4;
 #pragma unroll
-    for (int t = 0; t < (W4 ? kStage / 4 / kWave : kStage / kWave); ++t) {
-      const int f = t * kWave + lane;
-      if (t * kWave >= n) break;
-      if (f < n) {
-        if constexpr (W4) reinterpret_cast<float4 *>(sw)[f] = w4[t];
-        else sw[f] = w1[t];
-      }
+    for (int t = 0; t < NR; ++t) {
+      const int f = t * kWave + lane, h = f >> SWl, i = f & ((1 << SWl) - 1);
+      if (h < a.H) sw[h * pitch + i] = w[t];
     }
-    sx[lane] = x;
   }
 };
 
-// acc += sum over edges [b, e) of w X.  ONE: the whole wave takes one edge at
-// a time and its row's address is scalar work; else 64 >> Gl edges at once.
-// SAFE skips weights of 0, so that what such a row of X holds stays out.
-template <typename TX, int VW, bool PERM, bool ONE, bool W4, bool SAFE>
-__device__ inline void gather_rows(const SumArgs &a, const TX *X, int b, int e, int c, int head, int lane, float *sw,
-                                   int *sx, float (&acc)[VW]) {
-  constexpr int U = 8;
-  const int grp = ONE ? 0 : lane >> a.Gl, EPW = ONE ? 1 : kWave >> a.Gl;
-  Batch<PERM, W4> next;
-  next.fetch(a, b, e, lane);
+constexpr int kNarrow = 4;  // log2 of the edges staged where 64 do not fit
+template <int NR> constexpr int stage_floats() { return NR * 4 * ((1 << kNarrow) + 4); }
+
+// How the rows of X are addressed: one edge at a time with the wave's address
+// on the scalar unit; several with 32-bit byte offsets (X below 4 GB); several
+// with 64-bit products.
+enum { kScalar, kOffset, kLong };
+
+// acc += sum over edges [b, e) of w X; lanes of a group of SV take the vectors
+// of their slice, EPW groups an edge each.  Lanes without a vector read
+// nothing (a lookup of the vector cache serves four lanes: idle ones would
+// cost as much as others).  SAFE skips weights of 0, so that what such a row
+// of X holds stays out.
+template <typename TX, int VW, int MODE, int NR, bool SAFE>
+__device__ inline void gather_rows(const SumArgs &a, const TX *X, int b, int e, int c, int head, int grp, bool on,
+                                   int lane, float *sw, uint32_t *sx, float (&acc)[VW]) {
+  constexpr int U = MODE == kScalar ? 8 : 4;  // edges a group has in flight
+  const int step = MODE == kScalar ? U : a.EPW * U;
+  const uint32_t pitch = static_cast<uint32_t>(a.ldx * sizeof(TX));
+  const int SWl = a.H <= NR ? 6 : kNarrow;
+  const float *swh = sw + head * ((1 << SWl) + 4);
+  Batch<NR> next;
+  next.fetch(a, SWl, b, e, lane);
   for (int j0 = b; j0 < e; j0 += a.BE) {
-    next.stage(a, lane, sw, sx);
+    next.stage(a, SWl, lane, sw);
     const int x = next.x;
+    if constexpr (MODE == kOffset) sx[lane] = static_cast<uint32_t>(x) * pitch;
+    if constexpr (MODE == kLong) sx[lane] = x;
     wave_lds_order();
-    if (j0 + a.BE < e) next.fetch(a, j0 + a.BE, e, lane);  // under way while this batch is summed
+    if (j0 + a.BE < e) next.fetch(a, SWl, j0 + a.BE, e, lane);  // under way while this batch is summed
     const int n = min(a.BE, e - j0);
-    for (int i0 = 0; i0 < n; i0 += EPW * U) {
-      float v[U][VW], w[U];
+    for (int i0 = 0; i0 < n; i0 += step) {
+      const int i = MODE == kScalar ? i0 : i0 + grp * U;
+      if (on) {
+        Raw<TX, VW> v[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        int i, s;
-        if constexpr (ONE) {
-          i = i0 + u;
-          s = __builtin_amdgcn_readlane(x, i);
-        } else {
-          i = min(i0 + u * EPW + grp, a.BE - 1);
-          s = sx[i];
+        for (int u = 0; u < U; ++u) {
+          // byte offsets of 32 bits on a scalar base; the row's own offset goes
+          // to the base where a row is the wave's
+          const char *base = reinterpret_cast<const char *>(X);
+          uint32_t at = c * static_cast<uint32_t>(sizeof(TX));
+          if constexpr (MODE == kScalar)
+            base += scalar(static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(x, i + u))) * pitch);
+          else if constexpr (MODE == kOffset)
+            at += sx[i + u];
+          else
+            base += static_cast<uint64_t>(sx[i + u]) * pitch;
+          v[u].ld(reinterpret_cast<const TX *>(base + at));
         }
-        w[u] = sw[i * a.H + head];
-        if constexpr (!ONE)
-          if (i0 + u * EPW + grp >= a.BE) w[u] = 0.0f;
-        Vec<TX, VW>::ld(X + static_cast<int64_t>(s) * a.ldx + c, v[u]);
+        float w[U];
+#pragma unroll
+        for (int u = 0; u < U; u += 4) {
+          const float4 f = *reinterpret_cast<const float4 *>(swh + i + u);
+          w[u] = f.x;
+          w[u + 1] = f.y;
+          w[u + 2] = f.z;
+          w[u + 3] = f.w;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float r[VW];
+          v[u].get(r);
+#pragma unroll
+          for (int k = 0; k < VW; ++k) acc[k] = fmaf(w[u], SAFE && w[u] == 0.0f ? 0.0f : r[k], acc[k]);
+        }
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int k = 0; k < VW; ++k) acc[k] = fmaf(w[u], SAFE && w[u] == 0.0f ? 0.0f : v[u][k], acc[k]);
     }
     wave_lds_order();
   }
@@ -702,25 +929,17 @@ __device__ inline void gather_rows(const SumArgs &a, const TX *X, int b, int e, 
 
 // out[r] = scale sum over the row's edges of w[e][head] X[col[e]].  One wave
 // per (row or piece, slice of columns).
-template <typename TX, typename TO, int VW, bool PERM, bool ONE, bool W4>
+template <typename TX, typename TO, int VW, int MODE, int NR>
 __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const TX *__restrict__ X,
                                                               TO *__restrict__ out) {
-  __shared__ __align__(16) float sw[kWaves][kStage];
-  __shared__ int sx[kWaves][kWave];
-  // consecutive blocks go to the eight XCDs in turn: a slice stays on one XCD
-  // (S a multiple of 8), so each L2 holds an eighth of X
-  int slice, rb;
-  if (a.S <= 8) {
-    slice = blockIdx.x % a.S;
-    rb = blockIdx.x / a.S;
-  } else {
-    const int qd = blockIdx.x >> 3;
-    slice = (qd / a.blocks) * 8 + (blockIdx.x & 7);
-    rb = qd % a.blocks;
-  }
+  __shared__ __align__(16) float sw[kWaves][stage_floats<NR>()];
+  __shared__ __align__(16) uint32_t sx[kWaves][kWave];
+  const Slot sl = slot_of(a.S, a.blocks);
+  const int slice = sl.slice, rb = sl.block;
   const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x >> 6);
   const int unit = a.unit0 + rb * kWaves + wave;
-  if (unit >= a.units) return;
+  const int nv = a.width / VW;
+  if (unit >= a.units || slice * a.SV >= nv) return;
   int row, b, e;
   const int p = unit - a.n_rows;
   if (p < 0) {
@@ -728,7 +947,7 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const T
     row_bounds(a.ptr, row, a.E, &b, &e);
     if (e - b > a.T) return;
   } else {
-    const Piece pc = find_piece(p, a.T, a.ptr, a.n_rows, a.E, [&](int pos) { return owner<PERM>(a, pos); });
+    const Piece pc = find_piece(p, a.T, a.ptr, a.n_rows, a.E, [&](int pos) { return owner(a, pos); });
     if (pc.row < 0) return;
     row = pc.row;
     b = pc.begin;
@@ -736,16 +955,15 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const T
   }
   b = uniform(b);
   e = uniform(e);
-  const int gl = ONE ? lane : lane & ((1 << a.Gl) - 1);
-  const int nv = a.width / VW;
+  const int grp = MODE == kScalar ? 0 : lane / a.SV, gl = lane - grp * a.SV;
   const int vj = slice * a.SV + gl;
-  const bool on = gl < a.SV && vj < nv;
+  const bool on = gl < a.SV && grp < a.EPW && vj < nv;
   const int c = (on ? vj : nv - 1) * VW;
   const int head = (c % a.C) / a.Ch;
   float acc[VW];
 #pragma unroll
   for (int k = 0; k < VW; ++k) acc[k] = 0.0f;
-  gather_rows<TX, VW, PERM, ONE, W4, false>(a, X, b, e, c, head, lane, sw[wave], sx[wave], acc);
+  gather_rows<TX, VW, MODE, NR, false>(a, X, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
   // A sum that is finite had no infinity or NaN in it, so its weights of 0
   // added 0.  One that is not is taken again with those edges left out.
   bool odd = false;
@@ -754,13 +972,19 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const T
   if (__any(odd)) {
 #pragma unroll
     for (int k = 0; k < VW; ++k) acc[k] = 0.0f;
-    gather_rows<TX, VW, PERM, ONE, W4, true>(a, X, b, e, c, head, lane, sw[wave], sx[wave], acc);
+    gather_rows<TX, VW, MODE, NR, true>(a, X, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
   }
-  if constexpr (!ONE)
-    for (int o = 1 << a.Gl; o < kWave; o <<= 1)
+  if constexpr (MODE != kScalar) {
+    float sum[VW];
 #pragma unroll
-      for (int k = 0; k < VW; ++k) acc[k] += __shfl_xor(acc[k], o);
-  if (!on || (!ONE && (lane >> a.Gl) != 0)) return;
+    for (int k = 0; k < VW; ++k) sum[k] = acc[k];
+    for (int g = 1; g < a.EPW; ++g)
+#pragma unroll
+      for (int k = 0; k < VW; ++k) sum[k] += __shfl(acc[k], (gl + g * a.SV) & (kWave - 1));
+#pragma unroll
+    for (int k = 0; k < VW; ++k) acc[k] = sum[k];
+  }
+  if (!on || grp != 0) return;
   if (p >= 0) {
     Vec<float, VW>::st(a.part + static_cast<int64_t>(p) * a.width + c, acc);
     return;
@@ -772,12 +996,12 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const T
 
 // Long rows: the pieces' sums, added in edge order.  One block per window and
 // 256 columns; it acts for the long row that starts in its window, if any.
-template <typename TO, bool PERM>
+template <typename TO>
 __global__ void __launch_bounds__(kThreads) long_sum_kernel(SumArgs a, TO *__restrict__ out) {
   const int total = min(max(a.ptr[a.n_rows], 0), a.E);
   const int64_t w0 = static_cast<int64_t>(blockIdx.x) * a.T;
   if (w0 >= total) return;
-  const int row = owner<PERM>(a, static_cast<int>(min(w0 + a.T, static_cast<int64_t>(total)) - 1));
+  const int row = owner(a, static_cast<int>(min(w0 + a.T, static_cast<int64_t>(total)) - 1));
   if (row < 0 || row >= a.n_rows) return;
   int b, e;
   row_bounds(a.ptr, row, a.E, &b, &e);
@@ -786,7 +1010,14 @@ __global__ void __launch_bounds__(kThreads) long_sum_kernel(SumArgs a, TO *__res
   if (c >= a.width) return;
   const int n = piece_count(b, e, a.T);
   float s = 0.0f;
-  for (int i = 0; i < n; ++i) s += a.part[static_cast<int64_t>(piece_id(b, a.T, i)) * a.width + c];
+  for (int i0 = 0; i0 < n; i0 += 8) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      v[u] = a.part[static_cast<int64_t>(piece_id(b, a.T, min(i0 + u, n - 1))) * a.width + c];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s += i0 + u < n ? v[u] : 0.0f;
+  }
   Store<TO>::st(out + static_cast<int64_t>(row) * a.width + c, s * a.scale);
 }
 
@@ -798,7 +1029,7 @@ struct Shape {
   int n_dst, n_src, E;
   float scale;
   int t;         // dropout threshold
-  int T;         // edges of a row one block of the products holds
+  int T, TP;     // edges in a products block's LDS at a time; of a row one block takes
   int64_t pieces;
 };
 
@@ -827,6 +1058,7 @@ egnn_status make_shape_of(const egnn_attn_desc *d, const egnn_graph *g, Shape *s
   s->ldv = d->v_stride ? d->v_stride : vals;
   EGNN_REQUIRE(s->ldq >= qk && s->ldk >= qk, "q and k row strides must be 0 or at least 2 n_heads head_dim");
   EGNN_REQUIRE(s->ldv >= vals, "v row stride must be 0 or at least (lmax+1)^2 C");
+  EGNN_REQUIRE(s->ldq <= kMaxStride && s->ldk <= kMaxStride && s->ldv <= kMaxStride, "row strides are at most 2^29 elements");
   EGNN_REQUIRE(g, "graph is null");
   EGNN_REQUIRE(g->n_dst >= 0 && g->n_src >= 0, "negative row counts");
   EGNN_REQUIRE(g->n_edges >= 0, "negative edge count");
@@ -840,25 +1072,55 @@ egnn_status make_shape_of(const egnn_attn_desc *d, const egnn_graph *g, Shape *s
   s->E = static_cast<int>(g->n_edges);
   const int fit = 4096 / (2 * s->H);  // 16 KB of logits
   s->T = fit < 64 ? 64 : fit > 512 ? 512 : fit;
-  s->pieces = s->E > s->T ? 2 * ((static_cast<int64_t>(s->E) + s->T - 1) / s->T) : 0;
+  // Many rows fill the chip by themselves, and a piece costs a block that
+  // mostly finds nothing to do; few rows are cut at what LDS holds.
+  s->TP = s->n_dst >= 1024 ? 4096 : s->T;
+  s->pieces = s->E > s->TP ? 2 * ((static_cast<int64_t>(s->E) + s->TP - 1) / s->TP) : 0;
   return EGNN_OK;
 }
 
 struct SumPlan {
-  int nv, S, SV, Gl, T;
+  int S, SV, EPW, T;
   int64_t pieces;
 };
 
-// Slices and piece length of a weighted sum with rows of `nv` vectors.
-SumPlan sum_plan(int n_rows, int E, int nv) {
+// Slices and piece length of a weighted sum over rows of X of `nv` vectors of
+// `bytes` each.
+SumPlan sum_plan(int n_rows, int n_x, int E, int nv, int bytes) {
   SumPlan p;
-  p.nv = nv;
-  p.S = nv <= kWave ? 1 : 8 * ((nv + 8 * kWave - 1) / (8 * kWave));
-  p.SV = (nv + p.S - 1) / p.S;
-  p.Gl = log2_ceil(p.SV);
-  p.T = static_cast<int64_t>(n_rows) * p.S >= 4096 ? 2048 : 128;
+  if (nv <= kWave) {
+    p.S = 1;
+    p.SV = nv;
+  } else {
+    // slices in eights, one XCD each, in whole lookups (four vectors), narrow
+    // enough that an XCD's L2 (4 MB) holds its slice of X
+    int S = 8 * ((nv + 8 * kWave - 1) / (8 * kWave)), SV = kWave;
+    for (;; S += 8) {
+      SV = ((nv + S - 1) / S + 3) & ~3;
+      if (SV > kWave) continue;
+      if (SV <= kMinSlice || static_cast<int64_t>(n_x) * SV * bytes <= kSliceBytes) break;
+    }
+    if (static_cast<int64_t>(n_x) * SV * bytes > kSliceBytes) {  // too many rows for that: the widest slices
+      S = 8 * ((nv + 8 * kWave - 1) / (8 * kWave));
+      while ((SV = ((nv + S - 1) / S + 3) & ~3) > kWave) S += 8;
+    }
+    p.S = S;
+    p.SV = SV;
+  }
+  p.EPW = kWave / p.SV < 16 ? kWave / p.SV : 16;
+  p.T = static_cast<int64_t>(n_rows) * p.S >= 4096 ? 4096 : 128;
   p.pieces = E > p.T ? 2 * ((static_cast<int64_t>(E) + p.T - 1) / p.T) : 0;
   return p;
+}
+
+// Parts of a row's edges in the dot products with v: in eights, so that an
+// XCD's part of v fits its L2; one where that leaves too few edges a part to
+// pay for reading the row of grad_out again (8), or where rows are short.
+int dot_parts(const Shape &s, int bytes) {
+  const int64_t deg = s.E / (s.n_dst > 0 ? s.n_dst : 1);
+  const int64_t v = static_cast<int64_t>(s.n_src) * s.K * s.C * bytes;
+  const int64_t parts = 8 * ((v + 8 * kPartBytes - 1) / (8 * kPartBytes));
+  return parts * 8 <= deg ? static_cast<int>(parts) : deg >= 32 && s.n_dst < 1024 ? 8 : 1;
 }
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -873,15 +1135,16 @@ template <typename T> int vec_width(int Ch, int64_t ld, const void *p) {
 }
 
 struct Saved {
-  float *logits, *w;
+  float *logits;
   float2 *stats;
   int *dst;
 };
 
+int64_t plane(const Shape &s) { return (static_cast<int64_t>(s.E) + 63) & ~int64_t(63); }
+
 size_t saved_bytes_of(const Shape &s) {
   const size_t E = s.E, H = s.H;
-  return align256(E * 2 * H * 4) + align256(E * H * 4) + align256(static_cast<size_t>(s.n_dst) * 2 * H * 8) +
-         align256(E * 4);
+  return align256(E * 2 * H * 4) + align256(static_cast<size_t>(s.n_dst) * 2 * H * 8) + align256(E * 4);
 }
 
 Saved carve_saved(const Shape &s, char *p) {
@@ -889,8 +1152,6 @@ Saved carve_saved(const Shape &s, char *p) {
   Saved v;
   v.logits = reinterpret_cast<float *>(p);
   p += align256(E * 2 * H * 4);
-  v.w = reinterpret_cast<float *>(p);
-  p += align256(E * H * 4);
   v.stats = reinterpret_cast<float2 *>(p);
   p += align256(static_cast<size_t>(s.n_dst) * 2 * H * 8);
   v.dst = reinterpret_cast<int *>(p);
@@ -898,10 +1159,11 @@ Saved carve_saved(const Shape &s, char *p) {
 }
 
 // Pieces of a sum's partial rows: the most any vector width may ask for.
-size_t sum_part_bytes(int n_rows, int E, int width) {
+size_t sum_part_bytes(int n_rows, int n_x, int E, int width) {
   size_t most = 0;
-  for (int vw : {1, 4, 8}) {
-    const SumPlan p = sum_plan(n_rows, E, (width + vw - 1) / vw);
+  const int sizes[4][2] = {{1, 2}, {1, 4}, {4, 16}, {8, 16}};  // elements and bytes of a vector
+  for (const auto &z : sizes) {
+    const SumPlan p = sum_plan(n_rows, n_x, E, (width + z[0] - 1) / z[0], z[1]);
     const size_t n = align256(static_cast<size_t>(p.pieces) * width * 4);
     if (n > most) most = n;
   }
@@ -909,43 +1171,46 @@ size_t sum_part_bytes(int n_rows, int E, int width) {
 }
 
 size_t ws_fwd_of(const Shape &s, bool train) {
-  return (train ? 0 : saved_bytes_of(s)) + align256(static_cast<size_t>(s.pieces) * 2 * s.H * 8) +
-         sum_part_bytes(s.n_dst, s.E, s.K * s.C);
+  return (train ? 0 : saved_bytes_of(s)) + align256(plane(s) * s.H * 4) +
+         align256(static_cast<size_t>(s.pieces) * 2 * s.H * 8) + sum_part_bytes(s.n_dst, s.n_src, s.E, s.K * s.C);
 }
 
 size_t ws_bwd_of(const Shape &s) {
-  const size_t E = s.E, H = s.H;
-  size_t part = sum_part_bytes(s.n_dst, s.E, 2 * s.H * s.D);
+  const size_t E = s.E, H = s.H, P = plane(s);
+  size_t part = sum_part_bytes(s.n_dst, s.n_src, s.E, 2 * s.H * s.D);
   for (int width : {2 * s.H * s.D, s.K * s.C}) {
-    const size_t n = sum_part_bytes(s.n_src, s.E, width);
+    const size_t n = sum_part_bytes(s.n_src, s.n_dst, s.E, width);
     if (n > part) part = n;
   }
-  return align256(E * 2 * H * 4) + align256(static_cast<size_t>(s.n_dst) * H * 4) +
-         (s.pieces ? align256(E * H * 4) + align256(static_cast<size_t>(s.pieces) * H * 8) : 0) + part;
+  return align256(E * 2 * H * 4) + 2 * align256(E * H * 4) + 2 * align256(P * 2 * H * 4) + align256(P * H * 4) +
+         align256(E * 4) + align256(static_cast<size_t>(s.n_dst) * H * 4) +
+         align256(static_cast<size_t>(s.pieces) * H * 8) + part;
 }
 
-template <typename TX, typename TO, bool PERM>
-void launch_sum(unsigned grid, bool vec, bool one, bool w4, hipStream_t st, const SumArgs &a, const TX *X, TO *out) {
-  constexpr int V = 16 / sizeof(TX);
-  if (vec && one && w4) gather_sum_kernel<TX, TO, V, PERM, true, true><<<grid, kThreads, 0, st>>>(a, X, out);
-  else if (vec && one) gather_sum_kernel<TX, TO, V, PERM, true, false><<<grid, kThreads, 0, st>>>(a, X, out);
-  else if (vec && w4) gather_sum_kernel<TX, TO, V, PERM, false, true><<<grid, kThreads, 0, st>>>(a, X, out);
-  else if (vec) gather_sum_kernel<TX, TO, V, PERM, false, false><<<grid, kThreads, 0, st>>>(a, X, out);
-  else if (one) gather_sum_kernel<TX, TO, 1, PERM, true, false><<<grid, kThreads, 0, st>>>(a, X, out);
-  else gather_sum_kernel<TX, TO, 1, PERM, false, false><<<grid, kThreads, 0, st>>>(a, X, out);
+template <typename TX, typename TO, int VW, int NR>
+void launch_sum(unsigned grid, int mode, hipStream_t st, const SumArgs &a, const TX *X, TO *out) {
+  if (mode == kScalar) gather_sum_kernel<TX, TO, VW, kScalar, NR><<<grid, kThreads, 0, st>>>(a, X, out);
+  else if (mode == kOffset) gather_sum_kernel<TX, TO, VW, kOffset, NR><<<grid, kThreads, 0, st>>>(a, X, out);
+  else gather_sum_kernel<TX, TO, VW, kLong, NR><<<grid, kThreads, 0, st>>>(a, X, out);
 }
 
-template <typename TX, typename TO, bool PERM>
+template <typename TX, typename TO>
 egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream_t st) {
   if (a.n_rows == 0) return EGNN_OK;
   const int vw = vec_width<TX>(a.Ch, a.ldx, X) > 1 && aligned16(out) ? 16 / sizeof(TX) : 1;
-  const SumPlan p = sum_plan(a.n_rows, a.E, a.width / vw);
+  const SumPlan p = sum_plan(a.n_rows, a.n_x, a.E, a.width / vw, vw * static_cast<int>(sizeof(TX)));
   a.S = p.S;
   a.SV = p.SV;
-  a.Gl = p.Gl;
+  a.EPW = p.EPW;
   a.T = p.T;
+  // whole rounds of the edges in flight
+  const int round = p.EPW == 1 ? 8 : 4 * p.EPW, stage = a.H <= 16 ? kWave : 1 << kNarrow;
+  if (round > stage) a.EPW = stage / 4;
+  a.BE = stage / (a.EPW == 1 ? 8 : 4 * a.EPW) * (a.EPW == 1 ? 8 : 4 * a.EPW);
+  const int mode = a.EPW == 1                                                                       ? kScalar
+                   : static_cast<uint64_t>(a.n_x) * a.ldx * sizeof(TX) < (uint64_t(1) << 32) ? kOffset
+                                                                                                    : kLong;
   a.units = static_cast<int>(a.n_rows + p.pieces);
-  a.BE = a.H <= kStage / kWave ? kWave : kStage / kMaxHeads / 2;
   const int most = kMaxBlocks / a.S;  // blocks a slice in one launch
   for (a.unit0 = 0; a.unit0 < a.units; a.unit0 += most * kWaves) {
     Timed t(st, name, a.unit0 ? 0.0 : 2.0 * a.E * a.width,
@@ -955,36 +1220,33 @@ egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream
     const int left = (a.units - a.unit0 + kWaves - 1) / kWaves;
     a.blocks = left < most ? left : most;
     const unsigned grid = static_cast<unsigned>(a.blocks) * a.S;
-    launch_sum<TX, TO, PERM>(grid, vw > 1, p.Gl == 6, a.H % 4 == 0 && aligned16(a.w), st, a, X, out);
+    // registers for the next edges' weights: as few as the heads allow
+    if (vw > 1 && a.H <= 8) launch_sum<TX, TO, 16 / sizeof(TX), 8>(grid, mode, st, a, X, out);
+    else if (vw > 1) launch_sum<TX, TO, 16 / sizeof(TX), 16>(grid, mode, st, a, X, out);
+    else launch_sum<TX, TO, 1, 16>(grid, mode, st, a, X, out);
     EGNN_CHECK_LAUNCH();
   }
   if (p.pieces) {
     Timed t(st, "attn_long_sum", 0.0, 0.0);
-    long_sum_kernel<TO, PERM><<<dim3(static_cast<unsigned>(p.pieces / 2), ceil_div(a.width, kThreads)), kThreads, 0,
+    long_sum_kernel<TO><<<dim3(static_cast<unsigned>(p.pieces / 2), ceil_div(a.width, kThreads)), kThreads, 0,
                                 st>>>(a, out);
     EGNN_CHECK_LAUNCH();
   }
   return EGNN_OK;
 }
 
-template <typename T, int VW, bool ONE>
-void launch_logits(unsigned grid, size_t lds, int nit, hipStream_t st, const LogitArgs &a, const T *q, const T *k) {
-  if (nit <= 1) logits_kernel<T, VW, 1, ONE><<<grid, kThreads, lds, st>>>(a, q, k);
-  else if (nit <= 2) logits_kernel<T, VW, 2, ONE><<<grid, kThreads, lds, st>>>(a, q, k);
-  else logits_kernel<T, VW, 4, ONE><<<grid, kThreads, lds, st>>>(a, q, k);
+template <typename T, int VW, bool ONE, int NIT = kMaxNit>
+void launch_logits(unsigned grid, size_t lds, hipStream_t st, const LogitArgs &a, const T *q, const T *k) {
+  if constexpr (NIT > 1)
+    if (a.team.nit < NIT) return launch_logits<T, VW, ONE, NIT - 1>(grid, lds, st, a, q, k);
+  logits_kernel<T, VW, NIT, ONE><<<grid, kThreads, lds, st>>>(a, q, k);
 }
 
-template <typename T, int VW, bool ONE>
-void launch_logit_grad(unsigned grid, size_t lds, int nit, hipStream_t st, const GradArgs &a, const float *go,
-                       const T *v) {
-  if (nit <= 1) logit_grad_kernel<T, VW, 1, ONE><<<grid, kThreads, lds, st>>>(a, go, v);
-  else if (nit <= 4) logit_grad_kernel<T, VW, 4, ONE><<<grid, kThreads, lds, st>>>(a, go, v);
-  else logit_grad_kernel<T, VW, 8, ONE><<<grid, kThreads, lds, st>>>(a, go, v);
-}
-
-int rounds_of(int vectors, const Team &t) {
-  const int LT = 1 << t.LTl;
-  return (vectors + LT - 1) / LT;
+template <typename T, int VW, bool ONE, int NIT = kMaxNit>
+void launch_dots(unsigned grid, hipStream_t st, const DotArgs &a, const float *go, const T *v) {
+  if constexpr (NIT > 1)
+    if (a.team.nit < NIT) return launch_dots<T, VW, ONE, NIT - 1>(grid, st, a, go, v);
+  value_dots_kernel<T, VW, NIT, ONE><<<grid, kThreads, 0, st>>>(a, go, v);
 }
 
 template <typename T>
@@ -994,6 +1256,8 @@ egnn_status forward(const Shape &s, const egnn_graph *g, const T *q, const T *k,
   const bool train = saved != nullptr;
   const Saved sv = carve_saved(s, train ? static_cast<char *>(saved) : ws);
   if (!train) ws += saved_bytes_of(s);
+  auto *w = reinterpret_cast<float *>(ws);
+  ws += align256(plane(s) * s.H * 4);
   auto *piece_stats = reinterpret_cast<float2 *>(ws);
   ws += align256(static_cast<size_t>(s.pieces) * 2 * s.H * 8);
   if (s.n_dst == 0) return EGNN_OK;
@@ -1004,6 +1268,7 @@ egnn_status forward(const Shape &s, const egnn_graph *g, const T *q, const T *k,
   a.n_src = s.n_src;
   a.E = s.E;
   a.T = s.T;
+  a.TP = s.TP;
   a.H = s.H;
   a.D = s.D;
   a.ldq = s.ldq;
@@ -1013,27 +1278,27 @@ egnn_status forward(const Shape &s, const egnn_graph *g, const T *q, const T *k,
   a.mask = mask;
   a.lam = lam;
   a.drop = make_drop(rng, site, s.t);
-  a.logits = train || s.pieces ? sv.logits : nullptr;
-  a.w = sv.w;
+  a.logits = train || s.E > s.T ? sv.logits : nullptr;
+  a.w = w;
+  a.ldw = plane(s);
   a.stats = sv.stats;
   a.dst = sv.dst;
   a.piece_stats = piece_stats;
   if (s.E > 0) {
     constexpr int V = 16 / sizeof(T);
     const bool vec = vec_width<T>(s.D, s.ldq, q) > 1 && vec_width<T>(s.D, s.ldk, k) > 1;
-    const int vectors = vec ? s.D / V : s.D;
-    a.team = make_team(2 * s.H, vectors);
+    a.team = make_team(1, 2 * s.H, vec ? s.D / V : s.D);
+    a.Hpl = log2_ceil(2 * s.H);
     const unsigned grid = static_cast<unsigned>(s.n_dst + s.pieces);
     const size_t lds = static_cast<size_t>(s.T) * (2 * s.H + 1) * 4;
     {
       Timed t(st, "attn_logits", 4.0 * s.E * s.H * s.D,
               static_cast<double>(s.E) * (12.0 * s.H + 8 + (bias ? 8.0 * s.H : 0)) +
                   2.0 * s.H * s.D * sizeof(T) * (static_cast<double>(s.n_dst) + s.n_src));
-      const int nit = rounds_of(vectors, a.team);
-      const bool one = a.team.LTl + a.team.Hpl == 6;
-      if (vec && one) launch_logits<T, V, true>(grid, lds, nit, st, a, q, k);
-      else if (vec) launch_logits<T, V, false>(grid, lds, nit, st, a, q, k);
-      else launch_logits<T, 1, false>(grid, lds, nit, st, a, q, k);
+      const bool one = a.team.esh == 6;
+      if (vec && one) launch_logits<T, V, true>(grid, lds, st, a, q, k);
+      else if (vec) launch_logits<T, V, false>(grid, lds, st, a, q, k);
+      else launch_logits<T, 1, false>(grid, lds, st, a, q, k);
       EGNN_CHECK_LAUNCH();
     }
     if (s.pieces) {
@@ -1050,14 +1315,15 @@ egnn_status forward(const Shape &s, const egnn_graph *g, const T *q, const T *k,
   m.n_x = s.n_src;
   m.E = s.E;
   m.ldx = s.ldv;
-  m.w = sv.w;
+  m.w = w;
+  m.ldw = plane(s);
   m.H = s.H;
   m.C = s.C;
   m.Ch = s.C / s.H;
   m.width = s.K * s.C;
   m.scale = 1.0f;
   m.part = reinterpret_cast<float *>(ws);
-  return run_sum<T, T, false>(m, v, out, "attn_out", st);
+  return run_sum<T, T>(m, v, out, "attn_out", st);
 }
 
 template <typename T>
@@ -1065,57 +1331,85 @@ egnn_status backward(const Shape &s, const egnn_graph *g, const T *q, const T *k
                      const uint64_t *rng, uint32_t site, const void *saved, const float *go, float *gq, float *gk,
                      float *gv, float *glam, float *gbias, char *ws, hipStream_t st) {
   const Saved sv = carve_saved(s, static_cast<char *>(const_cast<void *>(saved)));
-  const size_t E = s.E, H = s.H;
-  float *dl = gbias ? gbias : reinterpret_cast<float *>(ws);
-  ws += align256(E * 2 * H * 4);
-  auto *t1 = reinterpret_cast<float *>(ws);
-  ws += align256(static_cast<size_t>(s.n_dst) * H * 4);
-  float *u = nullptr;
-  float2 *piece_t = nullptr;
-  if (s.pieces) {
-    u = reinterpret_cast<float *>(ws);
-    ws += align256(E * H * 4);
-    piece_t = reinterpret_cast<float2 *>(ws);
-    ws += align256(static_cast<size_t>(s.pieces) * H * 8);
-  }
+  const size_t E = s.E, H = s.H, P = plane(s);
+  const auto take = [&ws](size_t bytes) {
+    char *p = ws;
+    ws += align256(bytes);
+    return p;
+  };
+  auto *dl_rows = reinterpret_cast<float *>(take(E * 2 * H * 4));
+  float *dl = gbias ? gbias : dl_rows;
+  auto *u = reinterpret_cast<float *>(take(E * H * 4));
+  auto *wr = reinterpret_cast<float *>(take(E * H * 4));
+  auto *dlp = reinterpret_cast<float *>(take(P * 2 * H * 4));       // planes, by destination
+  auto *dlp_src = reinterpret_cast<float *>(take(P * 2 * H * 4));   // planes, by source
+  auto *w_src = reinterpret_cast<float *>(take(P * H * 4));
+  auto *dst_src = reinterpret_cast<int *>(take(E * 4));
+  auto *t1 = reinterpret_cast<float *>(take(static_cast<size_t>(s.n_dst) * H * 4));
+  auto *piece_t = reinterpret_cast<float2 *>(take(static_cast<size_t>(s.pieces) * H * 8));
   auto *part = reinterpret_cast<float *>(ws);
   constexpr int V = 16 / sizeof(T);
   const int Ch = s.C / s.H;
-  if (s.n_dst > 0) {
-    GradArgs a{};
+  if (s.E > 0) {
+    DotArgs a{};
     a.row_ptr = g->row_ptr;
     a.src = g->src;
     a.dst = sv.dst;
     a.n_dst = s.n_dst;
     a.n_src = s.n_src;
     a.E = s.E;
-    a.T = s.T;
     a.H = s.H;
     a.C = s.C;
     a.K = s.K;
     a.ldv = s.ldv;
+    a.u = u;
+    const bool vec = vec_width<T>(Ch, s.ldv, v) > 1 && aligned16(go);
+    a.team = make_team(s.K, s.H, vec ? Ch / V : Ch);
+    a.parts = dot_parts(s, sizeof(T));
+    a.T = static_cast<int64_t>(s.n_dst) * a.parts >= 4096 ? 4096 : 128;
+    const int64_t pieces = s.E > a.T ? 2 * ((static_cast<int64_t>(s.E) + a.T - 1) / a.T) : 0;
+    a.units = static_cast<int>(s.n_dst + pieces);
+    const int most = kMaxBlocks / a.parts;
+    for (a.unit0 = 0; a.unit0 < a.units; a.unit0 += most * kWaves) {
+      Timed t(st, "attn_value_dots", a.unit0 ? 0.0 : 2.0 * s.E * s.K * s.C,
+              a.unit0 ? 0.0
+                      : static_cast<double>(s.E) * (4.0 * s.H + 4) +
+                            static_cast<double>(s.K) * s.C * (4.0 * s.n_dst + sizeof(T) * static_cast<double>(s.n_src)));
+      const int left = (a.units - a.unit0 + kWaves - 1) / kWaves;
+      a.blocks = left < most ? left : most;
+      const unsigned grid = static_cast<unsigned>(a.blocks) * a.parts;
+      const bool one = a.team.esh == 6;
+      if (vec && one) launch_dots<T, V, true>(grid, st, a, go, v);
+      else if (vec) launch_dots<T, V, false>(grid, st, a, go, v);
+      else launch_dots<T, 1, false>(grid, st, a, go, v);
+      EGNN_CHECK_LAUNCH();
+    }
+  }
+  if (s.n_dst > 0) {
+    GradArgs a{};
+    a.row_ptr = g->row_ptr;
+    a.dst = sv.dst;
+    a.n_dst = s.n_dst;
+    a.E = s.E;
+    a.T = s.T;
+    a.TP = s.TP;
+    a.H = s.H;
+    a.Hpl = log2_ceil(s.H);
     a.lam = lam;
     a.drop = make_drop(rng, site, s.t);
     a.logits = reinterpret_cast<const float2 *>(sv.logits);
     a.stats = sv.stats;
     a.dl = reinterpret_cast<float2 *>(dl);
+    a.dlp = dlp;
+    a.ldw = plane(s);
+    a.wr = wr;
     a.t1 = t1;
     a.u = u;
     a.piece_t = piece_t;
-    const bool vec = vec_width<T>(Ch, s.ldv, v) > 1 && aligned16(go);
-    const int vectors = s.K * (vec ? Ch / V : Ch);
-    a.team = make_team(s.H, vectors);
-    const unsigned grid = static_cast<unsigned>(s.n_dst + s.pieces);
-    const size_t lds = static_cast<size_t>(s.T) * (s.H + 1) * 4;
     {
-      Timed t(st, "attn_logit_grad", 2.0 * s.E * s.K * s.C,
-              static_cast<double>(s.E) * (16.0 * s.H + 4) +
-                  static_cast<double>(s.K) * s.C * (4.0 * s.n_dst + sizeof(T) * static_cast<double>(s.n_src)));
-      const int nit = rounds_of(vectors, a.team);
-      const bool one = a.team.LTl + a.team.Hpl == 6;
-      if (vec && one) launch_logit_grad<T, V, true>(grid, lds, nit, st, a, go, v);
-      else if (vec) launch_logit_grad<T, V, false>(grid, lds, nit, st, a, go, v);
-      else launch_logit_grad<T, 1, false>(grid, lds, nit, st, a, go, v);
+      Timed t(st, "attn_logit_grad", 0.0, static_cast<double>(s.E) * 32.0 * s.H);
+      logit_grad_kernel<<<static_cast<unsigned>(s.n_dst + s.pieces), kThreads, static_cast<size_t>(s.T) * s.H * 4,
+                          st>>>(a);
       EGNN_CHECK_LAUNCH();
     }
     if (s.pieces) {
@@ -1129,6 +1423,17 @@ egnn_status backward(const Shape &s, const egnn_graph *g, const T *q, const T *k
     lam_grad_kernel<<<s.H, kThreads, 0, st>>>(t1, s.n_dst, s.H, glam);
     EGNN_CHECK_LAUNCH();
   }
+  if (s.E > 0) {
+    Timed t(st, "attn_regroup", 0.0, static_cast<double>(s.E) * (24.0 * s.H + 12));
+    const unsigned grid = ceil_div(s.E, kThreads);
+    if (s.H % 4 == 0 && aligned16(dl))
+      regroup_kernel<true><<<grid, kThreads, 0, st>>>(g->src_perm, g->src_ptr, s.n_src, s.E, s.H, sv.dst, wr, dl,
+                                                      plane(s), dst_src, w_src, dlp_src);
+    else
+      regroup_kernel<false><<<grid, kThreads, 0, st>>>(g->src_perm, g->src_ptr, s.n_src, s.E, s.H, sv.dst, wr, dl,
+                                                       plane(s), dst_src, w_src, dlp_src);
+    EGNN_CHECK_LAUNCH();
+  }
   SumArgs m{};
   m.ptr = g->row_ptr;
   m.col = g->src;
@@ -1137,32 +1442,34 @@ egnn_status backward(const Shape &s, const egnn_graph *g, const T *q, const T *k
   m.n_x = s.n_src;
   m.E = s.E;
   m.ldx = s.ldk;
-  m.w = dl;
+  m.w = dlp;
+  m.ldw = plane(s);
   m.H = 2 * s.H;
   m.C = 2 * s.H * s.D;
   m.Ch = s.D;
   m.width = 2 * s.H * s.D;
   m.scale = s.scale;
   m.part = part;
-  egnn_status r = run_sum<T, float, false>(m, k, gq, "attn_grad_q", st);
+  egnn_status r = run_sum<T, float>(m, k, gq, "attn_grad_q", st);
   if (r != EGNN_OK) return r;
   m.ptr = g->src_ptr;
-  m.perm = g->src_perm;
-  m.col = sv.dst;
+  m.col = dst_src;
   m.row_of = g->src;
+  m.perm = g->src_perm;
   m.n_rows = s.n_src;
   m.n_x = s.n_dst;
   m.ldx = s.ldq;
-  r = run_sum<T, float, true>(m, q, gk, "attn_grad_k", st);
+  m.w = dlp_src;
+  r = run_sum<T, float>(m, q, gk, "attn_grad_k", st);
   if (r != EGNN_OK) return r;
   m.ldx = static_cast<int64_t>(s.K) * s.C;
-  m.w = sv.w;
+  m.w = w_src;
   m.H = s.H;
   m.C = s.C;
   m.Ch = Ch;
   m.width = s.K * s.C;
   m.scale = 1.0f;
-  return run_sum<float, float, true>(m, go, gv, "attn_grad_v", st);
+  return run_sum<float, float>(m, go, gv, "attn_grad_v", st);
 }
 
 }  // namespace

@@ -440,20 +440,22 @@ struct LogitArgs {
   const float *lam;
   Drop drop;
   Team team;
-  float *logits;                  // [E][2H] or null (no backward, and no row beyond T)
+  float2 *maps;                   // [E][H] weights of both maps; logits until a row beyond T is done
+  bool keep;                      // the backward wants maps
   float *w;                       // [H][ldw]
   int64_t ldw;
-  float2 *stats;                  // [n_dst][2H]
   int *dst;                       // [E]
   float2 *piece_stats;            // [pieces][2H]
 };
 
-// Edge weights of [b, b + cnt) from their logits (in LDS or memory).
+// Edge weights of [b, b + cnt) from their logits (in LDS, or in a.maps).
 __device__ inline void edge_weights(const LogitArgs &a, const float2 *lg, const float2 *fin, int b, int cnt) {
+  float2 *maps = a.maps + static_cast<int64_t>(b) * a.H;
   for_decisions(b, cnt, a.H, a.drop, [&](int at, int i, int h, float m) {
     const float2 l = lg[at];
-    const float a0 = weight_of(l.x, fin[2 * h]), a1 = weight_of(l.y, fin[2 * h + 1]);
-    a.w[h * a.ldw + b + i] = m == 0.0f ? 0.0f : m * (a0 - a.lam[h] * a1);
+    const float2 al = make_float2(weight_of(l.x, fin[2 * h]), weight_of(l.y, fin[2 * h + 1]));
+    if (a.keep) maps[at] = al;
+    a.w[h * a.ldw + b + i] = m == 0.0f ? 0.0f : m * (al.x - a.lam[h] * al.y);
   });
 }
 
@@ -483,6 +485,7 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *
   }
   const int Hp = 1 << a.Hpl;
   const int col = threadIdx.x & (Hp - 1), r0 = threadIdx.x >> a.Hpl, R = kThreads >> a.Hpl;
+  const bool whole = p < 0 && e - b <= a.T;
   float M = -INFINITY, S = 0.0f;
   for (int c0 = b; c0 < e; c0 += a.T) {
     const int cnt = min(a.T, e - c0);
@@ -513,7 +516,7 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *
         }
         if (scol[i] < 0) l = -INFINITY;
         lg[i * H2 + col] = l;
-        if (a.logits) a.logits[o] = l;
+        if (!whole) reinterpret_cast<float *>(a.maps)[o] = l;
         Mc = fmaxf(Mc, l);
       }
     const float Mn = fmaxf(M, column_reduce(Mc, Hp, red, MaxOp()));
@@ -527,16 +530,10 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *
     if (r0 == 0 && col < H2) a.piece_stats[static_cast<int64_t>(p) * H2 + col] = make_float2(M, S);
     return;
   }
-  if (r0 == 0 && col < H2) {
-    const float2 st = finish_stats(M, S);
-    fin[col] = st;
-    a.stats[static_cast<int64_t>(d) * H2 + col] = st;
-  }
-  __syncthreads();
-  if (e - b <= a.T)
-    edge_weights(a, reinterpret_cast<const float2 *>(lg), fin, b, e - b);
-  else  // written by this block, so its own barrier and cache order them
-    edge_weights(a, reinterpret_cast<const float2 *>(a.logits) + static_cast<int64_t>(b) * a.H, fin, b, e - b);
+  if (r0 == 0 && col < H2) fin[col] = finish_stats(M, S);
+  __syncthreads();  // orders the logits that this block wrote to memory, too
+  edge_weights(a, whole ? reinterpret_cast<const float2 *>(lg) : a.maps + static_cast<int64_t>(b) * a.H, fin, b,
+               e - b);
 }
 
 // Long rows: the pieces' statistics joined, then their edge weights.
@@ -562,13 +559,9 @@ __global__ void __launch_bounds__(kThreads) long_weights_kernel(LogitArgs a) {
       if (st.x != -INFINITY) S += st.y * __expf(st.x - M);
     }
   S = column_reduce(S, Hp, red, SumOp());
-  if (r0 == 0 && col < H2) {
-    fin[col] = finish_stats(M, S);
-    if (pc.begin == b) a.stats[static_cast<int64_t>(pc.row) * H2 + col] = fin[col];
-  }
+  if (r0 == 0 && col < H2) fin[col] = finish_stats(M, S);
   __syncthreads();
-  edge_weights(a, reinterpret_cast<const float2 *>(a.logits) + static_cast<int64_t>(pc.begin) * a.H, fin, pc.begin,
-               pc.end - pc.begin);
+  edge_weights(a, a.maps + static_cast<int64_t>(pc.begin) * a.H, fin, pc.begin, pc.end - pc.begin);
 }
 
 struct DotArgs {
@@ -582,9 +575,11 @@ struct DotArgs {
 };
 
 // u[e][h] = <grad_out[d], v[src]> over the head's channels.  One wave per (row
-// or piece, part of its edges).  Part p of every row goes to XCD p % 8: rows
-// list their sources in ascending order, so a part meets about the same
-// stretch of v in every row, and the XCD's L2 holds it.
+// or piece, part of its edges).  Part p of every row goes to XCD p % 8 and
+// starts after as many edges as there are sources below p n_src / parts: a
+// partition of the row whatever its order, and where the sources ascend (as
+// egnn_build_graph writes them) the part's sources are one stretch of v, which
+// the XCD's L2 then holds for all rows.
 template <typename T, int VW, int NIT, bool ONE>
 __global__ void __launch_bounds__(kThreads) value_dots_kernel(DotArgs a, const float *__restrict__ go,
                                                               const T *__restrict__ v) {
@@ -604,9 +599,21 @@ __global__ void __launch_bounds__(kThreads) value_dots_kernel(DotArgs a, const f
     b = pc.begin;
     e = pc.end;
   }
-  const int64_t len = e - b;
-  e = uniform(b + static_cast<int>(len * (sl.slice + 1) / a.parts));
-  b = uniform(b + static_cast<int>(len * sl.slice / a.parts));
+  b = uniform(b);
+  e = uniform(e);
+  if (a.parts > 1) {
+    const int from = static_cast<int>(static_cast<int64_t>(a.n_src) * sl.slice / a.parts);
+    const int to = static_cast<int>(static_cast<int64_t>(a.n_src) * (sl.slice + 1) / a.parts);
+    int below = 0, upto = 0;
+    for (int c0 = b; c0 < e; c0 += kWave) {
+      const int s = c0 + lane < e ? a.src[c0 + lane] : INT32_MAX;
+      below += __popcll(__ballot(s < from));
+      upto += __popcll(__ballot(s < to));
+    }
+    // the first part starts at the row's start and the last ends at its end, whatever the sources are
+    e = sl.slice + 1 < a.parts ? uniform(b + upto) : e;
+    b = sl.slice > 0 ? uniform(b + below) : b;
+  }
   for (int c0 = b; c0 < e; c0 += kWave) {
     const int cnt = min(kWave, e - c0);
     const int s = lane < cnt ? a.src[c0 + lane] : -1;
@@ -628,37 +635,68 @@ struct GradArgs {
   int T, TP, Hpl;
   const float *lam;
   Drop drop;
-  const float2 *logits;  // [E][H] pairs of maps
-  const float2 *stats;   // [n_dst][H] pairs of (M, 1/S): two entries a head
+  const float2 *maps;    // [E][H] the forward's weights of both maps
   float2 *dl;            // [E][H] pairs: gradient of the logits before the scale
   float *dlp;            // the same as planes [2H][ldw]
   int64_t ldw;
-  float *wr;             // [E][H] the forward's weights, again
+  float *wr;             // [E][H] the forward's edge weights, again
   float *t1;             // [n_dst][H] sum_e a1 u
   float *u;              // [E][H] in: <grad_out, v>; where a row does not stay in LDS, m times that
   float2 *piece_t;       // [pieces][H] (sum a0 u, sum a1 u)
 };
 
-__device__ inline float2 weights_of(float2 l, const float4 st) {
-  return make_float2(weight_of(l.x, make_float2(st.x, st.y)), weight_of(l.y, make_float2(st.z, st.w)));
+// The logits' gradients of edges [c0, c0 + cnt), whose weights lie in al
+// (pitch 2H + 1) and u in us: rows first, then through al into planes.
+__device__ inline void logit_grads(const GradArgs &a, int c0, int cnt, const float2 *tt, float *al, const float *us) {
+  const int H = a.H, pitch = 2 * H + 1;
+  float2 *dl = a.dl + static_cast<int64_t>(c0) * H;
+  for (int f = threadIdx.x; f < cnt * H; f += kThreads) {
+    const int i = f / H, h = f - i * H;
+    float *w = al + i * pitch + 2 * h;
+    const float u = us[f];
+    // a weight of exactly 0 (masked) has no gradient, whatever the row of v holds
+    const float2 g = make_float2(w[0] == 0.0f ? 0.0f : w[0] * (u - tt[h].x),
+                                 w[1] == 0.0f ? 0.0f : -a.lam[h] * w[1] * (u - tt[h].y));
+    dl[f] = g;
+    w[0] = g.x;
+    w[1] = g.y;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & (kWave - 1);
+  for (int p = threadIdx.x >> 6; p < 2 * H; p += kWaves)
+    for (int i = lane; i < cnt; i += kWave) a.dlp[p * a.ldw + c0 + i] = al[i * pitch + p];
 }
 
-__device__ inline void logit_grads(const GradArgs &a, int64_t e, int h, float u, float2 t, const float4 *st) {
-  const float2 w = weights_of(a.logits[e * a.H + h], st[h]);
-  // a weight of exactly 0 (masked) has no gradient, whatever the row of v holds
-  const float2 g =
-      make_float2(w.x == 0.0f ? 0.0f : w.x * (u - t.x), w.y == 0.0f ? 0.0f : -a.lam[h] * w.y * (u - t.y));
-  a.dl[e * a.H + h] = g;
-  a.dlp[2 * h * a.ldw + e] = g.x;
-  a.dlp[(2 * h + 1) * a.ldw + e] = g.y;
+__device__ inline void load_maps(const GradArgs &a, int c0, int cnt, float *al) {
+  const int H = a.H, pitch = 2 * H + 1;
+  const float2 *maps = a.maps + static_cast<int64_t>(c0) * H;
+  for (int f = threadIdx.x; f < cnt * H; f += kThreads) {
+    const int i = f / H, h = f - i * H;
+    const float2 w = maps[f];
+    al[i * pitch + 2 * h] = w.x;
+    al[i * pitch + 2 * h + 1] = w.y;
+  }
+}
+
+// Rows and pieces of more than T edges: their gradients once the row's sums
+// are known.
+__device__ inline void logit_grads_again(const GradArgs &a, int b, int e, const float2 *tt, float *al, float *us) {
+  for (int c0 = b; c0 < e; c0 += a.T) {
+    const int cnt = min(a.T, e - c0);
+    __syncthreads();
+    load_maps(a, c0, cnt, al);
+    for (int f = threadIdx.x; f < cnt * a.H; f += kThreads) us[f] = a.u[static_cast<int64_t>(c0) * a.H + f];
+    __syncthreads();
+    logit_grads(a, c0, cnt, tt, al, us);
+  }
 }
 
 // One block per row (or piece): the softmax's backward for both maps, T edges
 // at a time.
 __global__ void __launch_bounds__(kThreads) logit_grad_kernel(GradArgs a) {
-  extern __shared__ float us[];  // [T][H]
+  extern __shared__ float al[];  // [T][2H + 1], then u [T][H]
+  float *us = al + a.T * (2 * a.H + 1);
   __shared__ float red[kWaves][kWave];
-  __shared__ float4 st[kMaxHeads];
   __shared__ float2 tt[kMaxHeads];
   int d, b, e;
   const int p = static_cast<int>(blockIdx.x) - a.n_dst;
@@ -677,30 +715,29 @@ __global__ void __launch_bounds__(kThreads) logit_grad_kernel(GradArgs a) {
     b = pc.begin;
     e = pc.end;
   }
-  const int H = a.H, Hp = 1 << a.Hpl;
+  const int H = a.H, Hp = 1 << a.Hpl, pitch = 2 * H + 1;
   const int h = threadIdx.x & (Hp - 1), r0 = threadIdx.x >> a.Hpl, R = kThreads >> a.Hpl;
-  if (threadIdx.x < static_cast<unsigned>(H))
-    st[threadIdx.x] = reinterpret_cast<const float4 *>(a.stats)[static_cast<int64_t>(d) * H + threadIdx.x];
-  const bool keep = p >= 0 || e - b > a.T;  // u does not stay in LDS until the row's sums are known
+  const bool again = p >= 0 || e - b > a.T;  // u does not stay in LDS until the row's sums are known
   float t0 = 0.0f, t1 = 0.0f;
   for (int c0 = b; c0 < e; c0 += a.T) {
     const int cnt = min(a.T, e - c0);
     const int64_t o0 = static_cast<int64_t>(c0) * H;
     __syncthreads();
-    for_decisions(c0, cnt, H, a.drop, [&](int at, int, int hd, float m) {
-      const float2 w = weights_of(a.logits[o0 + at], st[hd]);
-      a.wr[o0 + at] = m == 0.0f ? 0.0f : m * (w.x - a.lam[hd] * w.y);
+    load_maps(a, c0, cnt, al);
+    __syncthreads();
+    for_decisions(c0, cnt, H, a.drop, [&](int at, int i, int hd, float m) {
+      const float *w = al + i * pitch + 2 * hd;
+      a.wr[o0 + at] = m == 0.0f ? 0.0f : m * (w[0] - a.lam[hd] * w[1]);
       const float x = m == 0.0f ? 0.0f : m * a.u[o0 + at];
       us[at] = x;
-      if (keep) a.u[o0 + at] = x;
+      if (again) a.u[o0 + at] = x;
     });
     __syncthreads();
     if (h < H)
       for (int i = r0; i < cnt; i += R) {
-        const float2 w = weights_of(a.logits[o0 + i * H + h], st[h]);
-        const float x = us[i * H + h];
-        t0 += w.x == 0.0f ? 0.0f : w.x * x;
-        t1 += w.y == 0.0f ? 0.0f : w.y * x;
+        const float w0 = al[i * pitch + 2 * h], w1 = al[i * pitch + 2 * h + 1], x = us[i * H + h];
+        t0 += w0 == 0.0f ? 0.0f : w0 * x;
+        t1 += w1 == 0.0f ? 0.0f : w1 * x;
       }
   }
   t0 = column_reduce(t0, Hp, red, SumOp());
@@ -714,15 +751,15 @@ __global__ void __launch_bounds__(kThreads) logit_grad_kernel(GradArgs a) {
     a.t1[static_cast<int64_t>(d) * H + h] = t1;
   }
   __syncthreads();
-  if (h < H)
-    for (int i = b + r0; i < e; i += R)
-      logit_grads(a, i, h, keep ? a.u[static_cast<int64_t>(i) * H + h] : us[(i - b) * H + h], tt[h], st);
+  if (again) logit_grads_again(a, b, e, tt, al, us);
+  else logit_grads(a, b, e - b, tt, al, us);
 }
 
 // Long rows: the pieces' sums joined, then the logits' gradients.
 __global__ void __launch_bounds__(kThreads) long_grad_kernel(GradArgs a) {
+  extern __shared__ float al[];
+  float *us = al + a.T * (2 * a.H + 1);
   __shared__ float red[kWaves][kWave];
-  __shared__ float4 st[kMaxHeads];
   __shared__ float2 tt[kMaxHeads];
   const Piece pc = find_piece(blockIdx.x, a.TP, a.row_ptr, a.n_dst, a.E, [&](int pos) { return a.dst[pos]; });
   if (pc.row < 0) return;
@@ -730,8 +767,6 @@ __global__ void __launch_bounds__(kThreads) long_grad_kernel(GradArgs a) {
   row_bounds(a.row_ptr, pc.row, a.E, &b, &e);
   const int H = a.H, Hp = 1 << a.Hpl;
   const int h = threadIdx.x & (Hp - 1), r0 = threadIdx.x >> a.Hpl, R = kThreads >> a.Hpl;
-  if (threadIdx.x < static_cast<unsigned>(H))
-    st[threadIdx.x] = reinterpret_cast<const float4 *>(a.stats)[static_cast<int64_t>(pc.row) * H + threadIdx.x];
   const int n = piece_count(b, e, a.TP);
   float t0 = 0.0f, t1 = 0.0f;
   if (h < H)
@@ -747,20 +782,25 @@ __global__ void __launch_bounds__(kThreads) long_grad_kernel(GradArgs a) {
     if (pc.begin == b) a.t1[static_cast<int64_t>(pc.row) * H + h] = t1;
   }
   __syncthreads();
-  if (h < H)
-    for (int i = pc.begin + r0; i < pc.end; i += R)
-      logit_grads(a, i, h, a.u[static_cast<int64_t>(i) * H + h], tt[h], st);
+  logit_grads_again(a, pc.begin, pc.end, tt, al, us);
 }
 
 // grad_lam[h] = -sum_d t1[d][h], one block a head, in a fixed order
-__global__ void __launch_bounds__(kThreads) lam_grad_kernel(const float *__restrict__ t1, int n_dst, int H,
+__global__ void __launch_bounds__(1024) lam_grad_kernel(const float *__restrict__ t1, int n_dst, int H,
                                                             float *__restrict__ grad_lam) {
-  __shared__ double red[kThreads];
+  constexpr int N = 1024;
+  __shared__ double red[N];
   double s = 0.0;
-  for (int d = threadIdx.x; d < n_dst; d += kThreads) s += t1[static_cast<int64_t>(d) * H + blockIdx.x];
+  for (int d0 = threadIdx.x; d0 < n_dst; d0 += 8 * N) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = t1[static_cast<int64_t>(min(d0 + u * N, n_dst - 1)) * H + blockIdx.x];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s += d0 + u * N < n_dst ? v[u] : 0.0f;
+  }
   red[threadIdx.x] = s;
   __syncthreads();
-  for (int o = kThreads / 2; o > 0; o >>= 1) {
+  for (int o = N / 2; o > 0; o >>= 1) {
     if (threadIdx.x < static_cast<unsigned>(o)) red[threadIdx.x] += red[threadIdx.x + o];
     __syncthreads();
   }
@@ -824,40 +864,43 @@ __device__ inline int owner(const SumArgs &a, int pos) {
   return static_cast<unsigned>(ed) < static_cast<unsigned>(a.E) ? a.row_of[ed] : -1;
 }
 
-// A wave stages BE edges: each head's weights side by side (SW apart), so that
-// a lane reads four edges' weights at once, and the edges' rows of X.  NR
+// A wave stages BE edges: each head's weights side by side (a pitch apart), so
+// that a lane reads four edges' weights at once, and the edges' rows of X.  NR
 // registers a lane hold the next edges' weights on their way: 64 edges of up
-// to NR heads, or 16 edges of up to 4 NR.
-template <int NR> struct Batch {
+// to NR heads, or (NARROW) 16 edges of up to 4 NR.
+template <int NR, bool NARROW> struct Batch {
+  static constexpr int kEdges = NARROW ? 16 : kWave, kPitch = kEdges + 4;
+  static constexpr int kFloats = (NARROW ? 4 * NR : NR) * kPitch;
   int x;
   float w[NR];
 
   // Edges past the end and rows outside X have weight 0 and row 0.
-  __device__ inline void fetch(const SumArgs &a, int SWl, int j0, int e, int lane) {
+  __device__ inline void fetch(const SumArgs &a, int j0, int e, int lane) {
     x = -1;
     if (lane < a.BE && j0 + lane < e) x = a.col[j0 + lane];
     const bool live = static_cast<unsigned>(x) < static_cast<unsigned>(a.n_x);
     const uint64_t there = __ballot(live);
     x = live ? x : 0;
 #pragma unroll
-    for (int t = 0; t < NR; ++t) {
-      const int f = t * kWave + lane, h = f >> SWl, i = f & ((1 << SWl) - 1);
-      w[t] = h < a.H && ((there >> i) & 1) ? a.w[h * a.ldw + j0 + i] : 0.0f;
+    for (int t = 0; t < NR; ++t) w[t] = 0.0f;
+    if constexpr (NARROW) {
+      const int i = lane & 15, h0 = lane >> 4;
+      if ((there >> i) & 1)
+#pragma unroll
+        for (int t = 0; t < NR; ++t)
+          w[t] = a.w[min(4 * t + h0, a.H - 1) * a.ldw + j0 + i];
+    } else if (live) {
+      // plane t's address is the wave's; planes past the last are read again and not used
+#pragma unroll
+      for (int t = 0; t < NR; ++t) w[t] = (a.w + min(t, a.H - 1) * a.ldw + j0)[static_cast<uint32_t>(lane)];
     }
   }
 
-  __device__ inline void stage(const SumArgs &a, int SWl, int lane, float *sw) const {
-    const int pitch = (1 << SWl) + 4;
+  __device__ inline void stage(int lane, float *sw) const {
 #pragma unroll
-    for (int t = 0; t < NR; ++t) {
-      const int f = t * kWave + lane, h = f >> SWl, i = f & ((1 << SWl) - 1);
-      if (h < a.H) sw[h * pitch + i] = w[t];
-    }
+    for (int t = 0; t < NR; ++t) sw[(NARROW ? 4 * t + (lane >> 4) : t) * kPitch + (NARROW ? lane & 15 : lane)] = w[t];
   }
 };
-
-constexpr int kNarrow = 4;  // log2 of the edges staged where 64 do not fit
-template <int NR> constexpr int stage_floats() { return NR * 4 * ((1 << kNarrow) + 4); }
 
 // How the rows of X are addressed: one edge at a time with the wave's address
 // on the scalar unit; several with 32-bit byte offsets (X below 4 GB); several
@@ -869,28 +912,36 @@ enum { kScalar, kOffset, kLong };
 // nothing (a lookup of the vector cache serves four lanes: idle ones would
 // cost as much as others).  SAFE skips weights of 0, so that what such a row
 // of X holds stays out.
-template <typename TX, int VW, int MODE, int NR, bool SAFE>
+template <typename TX, int VW, int MODE, int NR, bool NARROW, bool SAFE>
 __device__ inline void gather_rows(const SumArgs &a, const TX *X, int b, int e, int c, int head, int grp, bool on,
                                    int lane, float *sw, uint32_t *sx, float (&acc)[VW]) {
   constexpr int U = MODE == kScalar ? 8 : 4;  // edges a group has in flight
   const int step = MODE == kScalar ? U : a.EPW * U;
   const uint32_t pitch = static_cast<uint32_t>(a.ldx * sizeof(TX));
-  const int SWl = a.H <= NR ? 6 : kNarrow;
-  const float *swh = sw + head * ((1 << SWl) + 4);
-  Batch<NR> next;
-  next.fetch(a, SWl, b, e, lane);
+  using B = Batch<NR, NARROW>;
+  const float *swh = sw + head * B::kPitch;
+  B next;
+  next.fetch(a, b, e, lane);
   for (int j0 = b; j0 < e; j0 += a.BE) {
-    next.stage(a, SWl, lane, sw);
+    next.stage(lane, sw);
     const int x = next.x;
     if constexpr (MODE == kOffset) sx[lane] = static_cast<uint32_t>(x) * pitch;
     if constexpr (MODE == kLong) sx[lane] = x;
     wave_lds_order();
-    if (j0 + a.BE < e) next.fetch(a, SWl, j0 + a.BE, e, lane);  // under way while this batch is summed
+    if (j0 + a.BE < e) next.fetch(a, j0 + a.BE, e, lane);  // under way while this batch is summed
     const int n = min(a.BE, e - j0);
     for (int i0 = 0; i0 < n; i0 += step) {
       const int i = MODE == kScalar ? i0 : i0 + grp * U;
       if (on) {
         Raw<TX, VW> v[U];
+        uint32_t rows[4] = {0, 0, 0, 0};
+        if constexpr (MODE != kScalar) {
+          const uint4 r = *reinterpret_cast<const uint4 *>(sx + i);
+          rows[0] = r.x;
+          rows[1] = r.y;
+          rows[2] = r.z;
+          rows[3] = r.w;
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           // byte offsets of 32 bits on a scalar base; the row's own offset goes
@@ -900,9 +951,9 @@ __device__ inline void gather_rows(const SumArgs &a, const TX *X, int b, int e, 
           if constexpr (MODE == kScalar)
             base += scalar(static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(x, i + u))) * pitch);
           else if constexpr (MODE == kOffset)
-            at += sx[i + u];
+            at += rows[u & 3];
           else
-            base += static_cast<uint64_t>(sx[i + u]) * pitch;
+            base += static_cast<uint64_t>(rows[u & 3]) * pitch;
           v[u].ld(reinterpret_cast<const TX *>(base + at));
         }
         float w[U];
@@ -929,10 +980,10 @@ __device__ inline void gather_rows(const SumArgs &a, const TX *X, int b, int e, 
 
 // out[r] = scale sum over the row's edges of w[e][head] X[col[e]].  One wave
 // per (row or piece, slice of columns).
-template <typename TX, typename TO, int VW, int MODE, int NR>
+template <typename TX, typename TO, int VW, int MODE, int NR, bool NARROW>
 __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const TX *__restrict__ X,
                                                               TO *__restrict__ out) {
-  __shared__ __align__(16) float sw[kWaves][stage_floats<NR>()];
+  __shared__ __align__(16) float sw[kWaves][Batch<NR, NARROW>::kFloats];
   __shared__ __align__(16) uint32_t sx[kWaves][kWave];
   const Slot sl = slot_of(a.S, a.blocks);
   const int slice = sl.slice, rb = sl.block;
@@ -963,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const T
   float acc[VW];
 #pragma unroll
   for (int k = 0; k < VW; ++k) acc[k] = 0.0f;
-  gather_rows<TX, VW, MODE, NR, false>(a, X, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
+  gather_rows<TX, VW, MODE, NR, NARROW, false>(a, X, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
   // A sum that is finite had no infinity or NaN in it, so its weights of 0
   // added 0.  One that is not is taken again with those edges left out.
   bool odd = false;
@@ -972,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const T
   if (__any(odd)) {
 #pragma unroll
     for (int k = 0; k < VW; ++k) acc[k] = 0.0f;
-    gather_rows<TX, VW, MODE, NR, true>(a, X, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
+    gather_rows<TX, VW, MODE, NR, NARROW, true>(a, X, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
   }
   if constexpr (MODE != kScalar) {
     float sum[VW];
@@ -1092,20 +1143,19 @@ SumPlan sum_plan(int n_rows, int n_x, int E, int nv, int bytes) {
     p.S = 1;
     p.SV = nv;
   } else {
-    // slices in eights, one XCD each, in whole lookups (four vectors), narrow
-    // enough that an XCD's L2 (4 MB) holds its slice of X
-    int S = 8 * ((nv + 8 * kWave - 1) / (8 * kWave)), SV = kWave;
-    for (;; S += 8) {
-      SV = ((nv + S - 1) / S + 3) & ~3;
-      if (SV > kWave) continue;
-      if (SV <= kMinSlice || static_cast<int64_t>(n_x) * SV * bytes <= kSliceBytes) break;
+    // slices in eights, one XCD each, in whole lookups (four vectors)
+    p.S = 8 * ((nv + 8 * kWave - 1) / (8 * kWave));
+    while ((p.SV = ((nv + p.S - 1) / p.S + 3) & ~3) > kWave) p.S += 8;
+    // Where an XCD's L2 (4 MB) does not hold its slice of X, narrower ones in
+    // whole lines (eight vectors) that it does hold, if there are such.
+    if (static_cast<int64_t>(n_x) * p.SV * bytes > kSliceBytes) {
+      int SV = (p.SV - 1) & ~7;
+      while (SV > kMinSlice && static_cast<int64_t>(n_x) * SV * bytes > kSliceBytes) SV -= 8;
+      if (SV >= kMinSlice && static_cast<int64_t>(n_x) * SV * bytes <= kSliceBytes) {
+        p.SV = SV;
+        p.S = 8 * ((nv + 8 * SV - 1) / (8 * SV));
+      }
     }
-    if (static_cast<int64_t>(n_x) * SV * bytes > kSliceBytes) {  // too many rows for that: the widest slices
-      S = 8 * ((nv + 8 * kWave - 1) / (8 * kWave));
-      while ((SV = ((nv + S - 1) / S + 3) & ~3) > kWave) S += 8;
-    }
-    p.S = S;
-    p.SV = SV;
   }
   p.EPW = kWave / p.SV < 16 ? kWave / p.SV : 16;
   p.T = static_cast<int64_t>(n_rows) * p.S >= 4096 ? 4096 : 128;
@@ -1135,8 +1185,7 @@ template <typename T> int vec_width(int Ch, int64_t ld, const void *p) {
 }
 
 struct Saved {
-  float *logits;
-  float2 *stats;
+  float2 *maps;
   int *dst;
 };
 
@@ -1144,16 +1193,14 @@ int64_t plane(const Shape &s) { return (static_cast<int64_t>(s.E) + 63) & ~int64
 
 size_t saved_bytes_of(const Shape &s) {
   const size_t E = s.E, H = s.H;
-  return align256(E * 2 * H * 4) + align256(static_cast<size_t>(s.n_dst) * 2 * H * 8) + align256(E * 4);
+  return align256(E * 2 * H * 4) + align256(E * 4);
 }
 
 Saved carve_saved(const Shape &s, char *p) {
   const size_t E = s.E, H = s.H;
   Saved v;
-  v.logits = reinterpret_cast<float *>(p);
+  v.maps = reinterpret_cast<float2 *>(p);
   p += align256(E * 2 * H * 4);
-  v.stats = reinterpret_cast<float2 *>(p);
-  p += align256(static_cast<size_t>(s.n_dst) * 2 * H * 8);
   v.dst = reinterpret_cast<int *>(p);
   return v;
 }
@@ -1187,11 +1234,11 @@ size_t ws_bwd_of(const Shape &s) {
          align256(static_cast<size_t>(s.pieces) * H * 8) + part;
 }
 
-template <typename TX, typename TO, int VW, int NR>
+template <typename TX, typename TO, int VW, int NR, bool NARROW>
 void launch_sum(unsigned grid, int mode, hipStream_t st, const SumArgs &a, const TX *X, TO *out) {
-  if (mode == kScalar) gather_sum_kernel<TX, TO, VW, kScalar, NR><<<grid, kThreads, 0, st>>>(a, X, out);
-  else if (mode == kOffset) gather_sum_kernel<TX, TO, VW, kOffset, NR><<<grid, kThreads, 0, st>>>(a, X, out);
-  else gather_sum_kernel<TX, TO, VW, kLong, NR><<<grid, kThreads, 0, st>>>(a, X, out);
+  if (mode == kScalar) gather_sum_kernel<TX, TO, VW, kScalar, NR, NARROW><<<grid, kThreads, 0, st>>>(a, X, out);
+  else if (mode == kOffset) gather_sum_kernel<TX, TO, VW, kOffset, NR, NARROW><<<grid, kThreads, 0, st>>>(a, X, out);
+  else gather_sum_kernel<TX, TO, VW, kLong, NR, NARROW><<<grid, kThreads, 0, st>>>(a, X, out);
 }
 
 template <typename TX, typename TO>
@@ -1204,7 +1251,7 @@ egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream
   a.EPW = p.EPW;
   a.T = p.T;
   // whole rounds of the edges in flight
-  const int round = p.EPW == 1 ? 8 : 4 * p.EPW, stage = a.H <= 16 ? kWave : 1 << kNarrow;
+  const int round = p.EPW == 1 ? 8 : 4 * p.EPW, stage = a.H <= 16 ? kWave : 16;
   if (round > stage) a.EPW = stage / 4;
   a.BE = stage / (a.EPW == 1 ? 8 : 4 * a.EPW) * (a.EPW == 1 ? 8 : 4 * a.EPW);
   const int mode = a.EPW == 1                                                                       ? kScalar
@@ -1221,9 +1268,12 @@ egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream
     a.blocks = left < most ? left : most;
     const unsigned grid = static_cast<unsigned>(a.blocks) * a.S;
     // registers for the next edges' weights: as few as the heads allow
-    if (vw > 1 && a.H <= 8) launch_sum<TX, TO, 16 / sizeof(TX), 8>(grid, mode, st, a, X, out);
-    else if (vw > 1) launch_sum<TX, TO, 16 / sizeof(TX), 16>(grid, mode, st, a, X, out);
-    else launch_sum<TX, TO, 1, 16>(grid, mode, st, a, X, out);
+    constexpr int V = 16 / sizeof(TX);
+    if (vw > 1 && a.H <= 8) launch_sum<TX, TO, V, 8, false>(grid, mode, st, a, X, out);
+    else if (vw > 1 && a.H <= 16) launch_sum<TX, TO, V, 16, false>(grid, mode, st, a, X, out);
+    else if (vw > 1) launch_sum<TX, TO, V, 16, true>(grid, mode, st, a, X, out);
+    else if (a.H <= 16) launch_sum<TX, TO, 1, 16, false>(grid, mode, st, a, X, out);
+    else launch_sum<TX, TO, 1, 16, true>(grid, mode, st, a, X, out);
     EGNN_CHECK_LAUNCH();
   }
   if (p.pieces) {
@@ -1278,10 +1328,10 @@ egnn_status forward(const Shape &s, const egnn_graph *g, const T *q, const T *k,
   a.mask = mask;
   a.lam = lam;
   a.drop = make_drop(rng, site, s.t);
-  a.logits = train || s.E > s.T ? sv.logits : nullptr;
+  a.maps = sv.maps;
+  a.keep = train;
   a.w = w;
   a.ldw = plane(s);
-  a.stats = sv.stats;
   a.dst = sv.dst;
   a.piece_stats = piece_stats;
   if (s.E > 0) {
@@ -1397,8 +1447,7 @@ egnn_status backward(const Shape &s, const egnn_graph *g, const T *q, const T *k
     a.Hpl = log2_ceil(s.H);
     a.lam = lam;
     a.drop = make_drop(rng, site, s.t);
-    a.logits = reinterpret_cast<const float2 *>(sv.logits);
-    a.stats = sv.stats;
+    a.maps = sv.maps;
     a.dl = reinterpret_cast<float2 *>(dl);
     a.dlp = dlp;
     a.ldw = plane(s);
@@ -1406,21 +1455,21 @@ egnn_status backward(const Shape &s, const egnn_graph *g, const T *q, const T *k
     a.t1 = t1;
     a.u = u;
     a.piece_t = piece_t;
+    const size_t lds = static_cast<size_t>(s.T) * (3 * s.H + 1) * 4;
     {
-      Timed t(st, "attn_logit_grad", 0.0, static_cast<double>(s.E) * 32.0 * s.H);
-      logit_grad_kernel<<<static_cast<unsigned>(s.n_dst + s.pieces), kThreads, static_cast<size_t>(s.T) * s.H * 4,
-                          st>>>(a);
+      Timed t(st, "attn_logit_grad", 0.0, static_cast<double>(s.E) * 36.0 * s.H);
+      logit_grad_kernel<<<static_cast<unsigned>(s.n_dst + s.pieces), kThreads, lds, st>>>(a);
       EGNN_CHECK_LAUNCH();
     }
     if (s.pieces) {
       Timed t(st, "attn_long_grad", 0.0, 0.0);
-      long_grad_kernel<<<static_cast<unsigned>(s.pieces), kThreads, 0, st>>>(a);
+      long_grad_kernel<<<static_cast<unsigned>(s.pieces), kThreads, lds, st>>>(a);
       EGNN_CHECK_LAUNCH();
     }
   }
   {
     Timed t(st, "attn_lam_grad", 0.0, 4.0 * s.n_dst * s.H);
-    lam_grad_kernel<<<s.H, kThreads, 0, st>>>(t1, s.n_dst, s.H, glam);
+    lam_grad_kernel<<<s.H, 1024, 0, st>>>(t1, s.n_dst, s.H, glam);
     EGNN_CHECK_LAUNCH();
   }
   if (s.E > 0) {

@@ -8,7 +8,9 @@ GPU, the calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as ct
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -425,9 +427,18 @@ def egnn_edge_update_bwd(desc, graph: Graph, geom, weights, x, buffers, grad_e_o
     return grad_x, grad_w
 
 
-def _on_one_device(named):
+def _as(t, dtype, shape):
+    """Whether t is just what a call reads: the quick form of _expect, which says what is wrong otherwise."""
+    return isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.is_contiguous()
+
+
+def _on_one_device(**tensors):
     """The GPU that every given tensor lives on (None entries are skipped)."""
-    dev = None
+    given = [t for t in tensors.values() if t is not None]
+    index = given[0].get_device()
+    if index >= 0 and all(t.get_device() == index for t in given):
+        return given[0].device
+    named, dev = tensors.items(), None
     for name, t in named:
         if t is None:
             continue
@@ -441,12 +452,40 @@ def _on_one_device(named):
 
 
 def _data(t):
-    return None if t is None else ct.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_HERE = contextlib.nullcontext()
+# the current stream's handle without building a torch.cuda.Stream (about 2 us a call)
+_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(dev):
+    """Makes dev the current device for a call; nothing to do where it is (torch.cuda.device costs about 2 us)."""
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _stream_of(dev):
+    return _handle(dev.index) if _handle is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _graph_struct(graph, grouped=False, dist=False):
+    """The fields that the attention and the bias read."""
+    g = _lib.EgnnGraph()
+    g.n_dst, g.n_src, g.n_edges = graph.n_dst, graph.n_src, graph.n_edges
+    if dist:
+        g.dist = graph.dist.data_ptr()
+        return g
+    g.row_ptr, g.src = graph.row_ptr.data_ptr(), graph.src.data_ptr()
+    if grouped:
+        g.src_ptr, g.src_perm = graph.src_ptr.data_ptr(), graph.src_perm.data_ptr()
+    return g
 
 
 def _expect_rng(rng, p):
     if rng is not None:
-        _expect(rng, "rng", torch.int64, (2,))
+        if not _as(rng, torch.int64, (2,)):
+            _expect(rng, "rng", torch.int64, (2,))
     elif not float(p) * 65536 < 0.5:
         raise ValueError("rng ({seed, step}, int64 on the GPU) is required when the dropout probability is not zero")
 
@@ -461,10 +500,16 @@ def attn_desc(lmax, C, n_heads, head_dim, scale=None, drop_p=0.0, site=0, storag
 def egnn_diff_attention_sizes(desc, graph: Graph):
     """(saved, inference workspace, training workspace) bytes."""
     s, i, t = ct.c_size_t(), ct.c_size_t(), ct.c_size_t()
-    g = graph.c_struct()
+    g = _lib.EgnnGraph()
+    g.n_dst, g.n_src, g.n_edges = graph.n_dst, graph.n_src, graph.n_edges
     _lib.check("egnn_diff_attention_sizes", _lib.load().egnn_diff_attention_sizes(
         ct.byref(desc), ct.byref(g), ct.byref(s), ct.byref(i), ct.byref(t)))
     return s.value, i.value, t.value
+
+
+def _attn_key(desc, graph):
+    """What the buffers' sizes depend on."""
+    return (desc.lmax, desc.C, desc.n_heads, desc.head_dim, graph.n_dst, graph.n_src, graph.n_edges)
 
 
 class AttnBuffers:
@@ -473,12 +518,24 @@ class AttnBuffers:
     def __init__(self, desc, graph: Graph, train=True):
         saved, infer, tr = egnn_diff_attention_sizes(desc, graph)
         dev = graph.row_ptr.device
+        self._fits = _attn_key(desc, graph)
         self.saved = torch.empty(max(saved, 1), dtype=torch.uint8, device=dev) if train else None
         self.ws = torch.empty(max(tr if train else infer, 1), dtype=torch.uint8, device=dev)
 
 
+def _check_attn_buffers(desc, graph, buffers):
+    if buffers._fits == _attn_key(desc, graph):
+        return
+    saved, infer, train = egnn_diff_attention_sizes(desc, graph)
+    if buffers.saved is not None:
+        _expect_bytes(buffers.saved, "buffers.saved", saved)
+    _expect_bytes(buffers.ws, "buffers.ws", infer if buffers.saved is None else train)
+
+
 def _expect_rows(t, name, dtype, shape, rows):
-    """Rows whose elements are packed, any distance apart; returns that distance in elements."""
+    """Rows whose elements are packed, any distance apart; returns that distance in elements (0: packed rows)."""
+    if _as(t, dtype, (rows, *shape)):
+        return 0
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a torch tensor")
     if t.dtype != dtype:
@@ -500,13 +557,17 @@ def _expect_rows(t, name, dtype, shape, rows):
 
 
 def _expect_graph(graph: Graph, grouped=False):
-    _expect(graph.row_ptr, "graph.row_ptr", torch.int32, (graph.n_dst + 1,))
-    _expect(graph.src, "graph.src", torch.int32, (None,), min_rows=graph.n_edges)
+    if not _as(graph.row_ptr, torch.int32, (graph.n_dst + 1,)):
+        _expect(graph.row_ptr, "graph.row_ptr", torch.int32, (graph.n_dst + 1,))
+    if not _as(graph.src, torch.int32, (graph.n_edges,)):
+        _expect(graph.src, "graph.src", torch.int32, (None,), min_rows=graph.n_edges)
     if grouped:
         if graph.src_ptr is None or graph.src_perm is None:
             raise ValueError("the backward needs the graph grouped by source (egnn_group_sources)")
-        _expect(graph.src_ptr, "graph.src_ptr", torch.int32, (graph.n_src + 1,))
-        _expect(graph.src_perm, "graph.src_perm", torch.int32, (None,), min_rows=graph.n_edges)
+        if not _as(graph.src_ptr, torch.int32, (graph.n_src + 1,)):
+            _expect(graph.src_ptr, "graph.src_ptr", torch.int32, (graph.n_src + 1,))
+        if not _as(graph.src_perm, torch.int32, (graph.n_edges,)):
+            _expect(graph.src_perm, "graph.src_perm", torch.int32, (None,), min_rows=graph.n_edges)
 
 
 def _check_attn(desc, graph: Graph, q, k, v, lam, rng, grouped=False):
@@ -515,13 +576,15 @@ def _check_attn(desc, graph: Graph, q, k, v, lam, rng, grouped=False):
         raise ValueError(f"unknown storage type {desc.storage}")
     dt, H, D, C, K = _STORAGE[desc.storage], desc.n_heads, desc.head_dim, desc.C, (desc.lmax + 1) ** 2
     _expect_graph(graph, grouped)
-    d = _lib.EgnnAttnDesc.from_buffer_copy(desc)
-    d.q_stride = _expect_rows(q, "q", dt, (H, 2, D), graph.n_dst)
-    d.k_stride = _expect_rows(k, "k", dt, (H, 2, D), graph.n_src)
-    d.v_stride = _expect_rows(v, "v", dt, (K, C), graph.n_src)
-    _expect(lam, "lam", torch.float32, (H,))
+    strides = (_expect_rows(q, "q", dt, (H, 2, D), graph.n_dst), _expect_rows(k, "k", dt, (H, 2, D), graph.n_src),
+               _expect_rows(v, "v", dt, (K, C), graph.n_src))
+    if not _as(lam, torch.float32, (H,)):
+        _expect(lam, "lam", torch.float32, (H,))
     _expect_rng(rng, desc.drop_p)
-    return d, K, dt
+    if strides != (desc.q_stride, desc.k_stride, desc.v_stride):
+        desc = _lib.EgnnAttnDesc.from_buffer_copy(desc)
+        desc.q_stride, desc.k_stride, desc.v_stride = strides
+    return desc, K, dt
 
 
 def egnn_diff_attention_fwd(desc, graph: Graph, q, k, v, lam, bias=None, mask=None, rng=None, out=None, buffers=None):
@@ -537,30 +600,27 @@ def egnn_diff_attention_fwd(desc, graph: Graph, q, k, v, lam, bias=None, mask=No
     lib = _lib.load()
     d, K, dt = _check_attn(desc, graph, q, k, v, lam, rng)
     E, H = graph.n_edges, desc.n_heads
-    if bias is not None:
+    if bias is not None and not _as(bias, torch.float32, (E, 2 * H)):
         _expect(bias.reshape(-1) if isinstance(bias, torch.Tensor) and bias.is_contiguous() else bias, "bias",
                 torch.float32, (E * 2 * H,))
-    if mask is not None:
+    if mask is not None and not _as(mask, torch.uint8, (E,)):
         if isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
             mask = mask.view(torch.uint8)
         _expect(mask, "mask", torch.uint8, (E,))
-    dev = _on_one_device([("graph.row_ptr", graph.row_ptr), ("graph.src", graph.src), ("q", q), ("k", k), ("v", v),
-                          ("lam", lam), ("bias", bias), ("mask", mask), ("rng", rng), ("out", out)]
-                         + ([("buffers.saved", buffers.saved), ("buffers.ws", buffers.ws)] if buffers else []))
-    with torch.cuda.device(dev):
+    dev = _on_one_device(row_ptr=graph.row_ptr, src=graph.src, q=q, k=k, v=v, lam=lam, bias=bias, mask=mask, rng=rng,
+                         out=out, saved=buffers.saved if buffers else None, ws=buffers.ws if buffers else None)
+    with _on(dev):
         if buffers is None:
             buffers = AttnBuffers(desc, graph, train=False)
-        saved, infer, train = egnn_diff_attention_sizes(d, graph)
-        if buffers.saved is not None:
-            _expect_bytes(buffers.saved, "buffers.saved", saved)
-        _expect_bytes(buffers.ws, "buffers.ws", infer if buffers.saved is None else train)
+        _check_attn_buffers(d, graph, buffers)
         if out is None:
             out = torch.empty((graph.n_dst, K, desc.C), dtype=dt, device=dev)
-        _expect(out, "out", dt, (graph.n_dst, K, desc.C))
-        g = graph.c_struct()
+        else:
+            _expect(out, "out", dt, (graph.n_dst, K, desc.C))
+        g = _graph_struct(graph)
         _lib.check("egnn_diff_attention_fwd", lib.egnn_diff_attention_fwd(
             ct.byref(d), ct.byref(g), _data(q), _data(k), _data(v), _data(lam), _data(bias), _data(mask), _data(rng),
-            _data(out), _data(buffers.saved), _data(buffers.ws), buffers.ws.numel(), _stream()))
+            _data(out), _data(buffers.saved), _data(buffers.ws), buffers.ws.numel(), _stream_of(dev)))
     return out, buffers
 
 
@@ -573,28 +633,25 @@ def egnn_diff_attention_bwd(desc, graph: Graph, q, k, v, lam, buffers, grad_out,
     lib = _lib.load()
     d, K, _ = _check_attn(desc, graph, q, k, v, lam, rng, grouped=True)
     E, H, D, C = graph.n_edges, desc.n_heads, desc.head_dim, desc.C
-    _expect(grad_out, "grad_out", torch.float32, (graph.n_dst, K, C))
+    if not _as(grad_out, torch.float32, (graph.n_dst, K, C)):
+        _expect(grad_out, "grad_out", torch.float32, (graph.n_dst, K, C))
     if buffers is None or buffers.saved is None:
         raise ValueError("the backward needs buffers made with train=True")
-    dev = _on_one_device([("graph.row_ptr", graph.row_ptr), ("graph.src", graph.src), ("graph.src_ptr", graph.src_ptr),
-                          ("graph.src_perm", graph.src_perm), ("q", q), ("k", k), ("v", v), ("lam", lam),
-                          ("rng", rng), ("grad_out", grad_out), ("buffers.saved", buffers.saved),
-                          ("buffers.ws", buffers.ws)])
-    with torch.cuda.device(dev):
-        saved, _, train = egnn_diff_attention_sizes(d, graph)
-        _expect_bytes(buffers.saved, "buffers.saved", saved)
-        _expect_bytes(buffers.ws, "buffers.ws", train)
+    dev = _on_one_device(row_ptr=graph.row_ptr, src=graph.src, src_ptr=graph.src_ptr, src_perm=graph.src_perm, q=q,
+                         k=k, v=v, lam=lam, rng=rng, grad_out=grad_out, saved=buffers.saved, ws=buffers.ws)
+    with _on(dev):
+        _check_attn_buffers(d, graph, buffers)
         f32 = dict(dtype=torch.float32, device=dev)
         gq = torch.empty((graph.n_dst, H, 2, D), **f32)
         gk = torch.empty((graph.n_src, H, 2, D), **f32)
         gv = torch.empty((graph.n_src, K, C), **f32)
         gl = torch.empty(H, **f32)
         gb = torch.empty((E, 2 * H), **f32)
-        g = graph.c_struct()
+        g = _graph_struct(graph, grouped=True)
         _lib.check("egnn_diff_attention_bwd", lib.egnn_diff_attention_bwd(
             ct.byref(d), ct.byref(g), _data(q), _data(k), _data(v), _data(lam), _data(rng), _data(buffers.saved),
             _data(grad_out), _data(gq), _data(gk), _data(gv), _data(gl), _data(gb), _data(buffers.ws),
-            buffers.ws.numel(), _stream()))
+            buffers.ws.numel(), _stream_of(dev)))
     return gq, gk, gv, gl, gb
 
 
@@ -608,8 +665,10 @@ def egnn_distance_borders(n_buckets, n_linear, r_linear, r_max):
 
 
 def _check_bias(graph: Graph, borders, n_buckets, n_columns):
-    _expect(borders, "borders", torch.float32, (n_buckets - 1,))
-    _expect(graph.dist, "graph.dist", torch.float32, (None,), min_rows=graph.n_edges)
+    if not _as(borders, torch.float32, (n_buckets - 1,)):
+        _expect(borders, "borders", torch.float32, (n_buckets - 1,))
+    if not _as(graph.dist, torch.float32, (graph.n_edges,)):
+        _expect(graph.dist, "graph.dist", torch.float32, (None,), min_rows=graph.n_edges)
     return _lib.EgnnBiasDesc(n_buckets, n_columns)
 
 
@@ -620,35 +679,42 @@ def egnn_distance_bias_fwd(graph: Graph, borders, table, out=None):
     d = _check_bias(graph, borders, B, M)
     if out is not None:
         _expect(out, "out", torch.float32, (graph.n_edges, M))
-    dev = _on_one_device([("graph.dist", graph.dist), ("borders", borders), ("table", table), ("out", out)])
-    with torch.cuda.device(dev):
+    dev = _on_one_device(dist=graph.dist, borders=borders, table=table, out=out)
+    with _on(dev):
         if out is None:
             out = torch.empty((graph.n_edges, M), dtype=torch.float32, device=dev)
-        g = graph.c_struct()
+        g = _graph_struct(graph, dist=True)
         _lib.check("egnn_distance_bias_fwd", _lib.load().egnn_distance_bias_fwd(
-            ct.byref(d), ct.byref(g), _data(borders), _data(table), _data(out), _stream()))
+            ct.byref(d), ct.byref(g), _data(borders), _data(table), _data(out), _stream_of(dev)))
     return out
+
+
+@functools.lru_cache(maxsize=64)
+def _bias_workspace(n_buckets, n_columns, n_edges):
+    """Workspace bytes of the table's gradient: they depend on the sizes alone."""
+    d, g, nbytes = _lib.EgnnBiasDesc(n_buckets, n_columns), _lib.EgnnGraph(), ct.c_size_t()
+    g.n_edges, g.dist = n_edges, 16   # any address: the query reads nothing
+    _lib.check("egnn_distance_bias_workspace",
+               _lib.load().egnn_distance_bias_workspace(ct.byref(d), ct.byref(g), ct.byref(nbytes)))
+    return nbytes.value
 
 
 def egnn_distance_bias_bwd(graph: Graph, borders, grad_bias):
     """grad_table [n_buckets][n_columns]: grad_bias [E][n_columns] summed over each bucket's edges."""
-    lib = _lib.load()
     _expect(grad_bias, "grad_bias", torch.float32, (graph.n_edges, None))
     if not isinstance(borders, torch.Tensor):
         raise ValueError("borders must be a torch tensor")
     B, M = borders.numel() + 1, grad_bias.shape[1]
     d = _check_bias(graph, borders, B, M)
-    dev = _on_one_device([("graph.dist", graph.dist), ("borders", borders), ("grad_bias", grad_bias)])
-    with torch.cuda.device(dev):
-        g = graph.c_struct()
-        nbytes = ct.c_size_t()
-        _lib.check("egnn_distance_bias_workspace",
-                   lib.egnn_distance_bias_workspace(ct.byref(d), ct.byref(g), ct.byref(nbytes)))
-        ws = torch.empty(max(nbytes.value, 1), dtype=torch.uint8, device=dev)
+    dev = _on_one_device(dist=graph.dist, borders=borders, grad_bias=grad_bias)
+    nbytes = _bias_workspace(B, M, graph.n_edges)
+    with _on(dev):
+        g = _graph_struct(graph, dist=True)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         out = torch.empty((B, M), dtype=torch.float32, device=dev)
-        _lib.check("egnn_distance_bias_bwd", lib.egnn_distance_bias_bwd(
-            ct.byref(d), ct.byref(g), _data(borders), _data(grad_bias), _data(out), _data(ws), nbytes.value,
-            _stream()))
+        _lib.check("egnn_distance_bias_bwd", _lib.load().egnn_distance_bias_bwd(
+            ct.byref(d), ct.byref(g), _data(borders), _data(grad_bias), _data(out), _data(ws), nbytes,
+            _stream_of(dev)))
     return out
 
 
@@ -668,17 +734,17 @@ def egnn_dropout_fwd(desc, x, rng, residual=None, out=None):
         raise ValueError(f"unknown storage type {desc.storage}")
     dt, shape = _STORAGE[desc.storage], (None, (desc.lmax + 1) ** 2, desc.C)
     _expect(x, "x", dt, shape)
-    if residual is not None:
+    if residual is not None and not _as(residual, dt, x.shape):
         _expect(residual, "residual", dt, tuple(x.shape))
     if out is not None:
         _expect(out, "out", dt, tuple(x.shape))
     _expect_rng(rng, desc.p)
-    dev = _on_one_device([("x", x), ("residual", residual), ("rng", rng), ("out", out)])
-    with torch.cuda.device(dev):
+    dev = _on_one_device(x=x, residual=residual, rng=rng, out=out)
+    with _on(dev):
         if out is None:
             out = torch.empty_like(x)
         _lib.check("egnn_dropout_fwd", _lib.load().egnn_dropout_fwd(
-            ct.byref(desc), x.shape[0], _data(x), _data(residual), _data(rng), _data(out), _stream()))
+            ct.byref(desc), x.shape[0], _data(x), _data(residual), _data(rng), _data(out), _stream_of(dev)))
     return out
 
 
@@ -688,12 +754,12 @@ def egnn_dropout_bwd(desc, grad_y, rng, out=None):
     if out is not None:
         _expect(out, "out", torch.float32, tuple(grad_y.shape))
     _expect_rng(rng, desc.p)
-    dev = _on_one_device([("grad_y", grad_y), ("rng", rng), ("out", out)])
-    with torch.cuda.device(dev):
+    dev = _on_one_device(grad_y=grad_y, rng=rng, out=out)
+    with _on(dev):
         if out is None:
             out = torch.empty_like(grad_y)
         _lib.check("egnn_dropout_bwd", _lib.load().egnn_dropout_bwd(
-            ct.byref(desc), grad_y.shape[0], _data(grad_y), _data(rng), _data(out), _stream()))
+            ct.byref(desc), grad_y.shape[0], _data(grad_y), _data(rng), _data(out), _stream_of(dev)))
     return out
 
 

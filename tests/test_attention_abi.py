@@ -55,8 +55,8 @@ def test_attention_size_queries(lib):
     ok, small = _sizes(lib, _attn(), _fake_graph(100, 100, 1000))
     ok2, large = _sizes(lib, _attn(), _fake_graph(100, 100, 2000))
     assert ok == 0 and ok2 == 0
-    # per edge and head two logits and a weight, per edge a row index
-    assert abs(large[0] - small[0] - 1000 * (8 * 12 + 4)) < 1024
+    # per edge and head the weights of both maps, per edge a row index
+    assert abs(large[0] - small[0] - 1000 * (8 * 8 + 4)) < 1024
     assert large[1] >= large[0] and large[2] > 0
 
 

@@ -507,17 +507,21 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *
     __syncthreads();
     float Mc = -INFINITY;
     if (col < H2)
-      for (int i = r0; i < cnt; i += R) {
-        const int64_t o = static_cast<int64_t>(c0 + i) * H2 + col;
-        float l = lg[i * H2 + col] * a.scale;
-        if (a.bias) {
-          const float bv = a.bias[o];
-          l = bv == -INFINITY ? -INFINITY : l + bv;  // a bias of -inf masks, whatever the product is
+      for (int i0 = r0; i0 < cnt; i0 += 4 * R) {
+        const int64_t o = static_cast<int64_t>(c0) * H2 + col;
+        float bv[4];  // loaded together; places past the end are clamped
+#pragma unroll
+        for (int u = 0; u < 4; ++u) bv[u] = a.bias ? a.bias[o + min(i0 + u * R, cnt - 1) * H2] : 0.0f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * R;
+          if (i >= cnt) break;
+          float l = lg[i * H2 + col] * a.scale + bv[u];
+          if (bv[u] == -INFINITY || scol[i] < 0) l = -INFINITY;  // masked, whatever the product is
+          lg[i * H2 + col] = l;
+          if (!whole) reinterpret_cast<float *>(a.maps)[o + i * H2] = l;
+          Mc = fmaxf(Mc, l);
         }
-        if (scol[i] < 0) l = -INFINITY;
-        lg[i * H2 + col] = l;
-        if (!whole) reinterpret_cast<float *>(a.maps)[o] = l;
-        Mc = fmaxf(Mc, l);
       }
     const float Mn = fmaxf(M, column_reduce(Mc, Hp, red, MaxOp()));
     float Sc = 0.0f;
@@ -785,39 +789,41 @@ __global__ void __launch_bounds__(kThreads) long_grad_kernel(GradArgs a) {
   logit_grads_again(a, pc.begin, pc.end, tt, al, us);
 }
 
-// grad_lam[h] = -sum_d t1[d][h], one block a head, in a fixed order
-__global__ void __launch_bounds__(1024) lam_grad_kernel(const float *__restrict__ t1, int n_dst, int H,
-                                                            float *__restrict__ grad_lam) {
-  constexpr int N = 1024;
-  __shared__ double red[N];
-  double s = 0.0;
-  for (int d0 = threadIdx.x; d0 < n_dst; d0 += 8 * N) {
-    float v[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = t1[static_cast<int64_t>(min(d0 + u * N, n_dst - 1)) * H + blockIdx.x];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) s += d0 + u * N < n_dst ? v[u] : 0.0f;
-  }
-  red[threadIdx.x] = s;
-  __syncthreads();
-  for (int o = N / 2; o > 0; o >>= 1) {
-    if (threadIdx.x < static_cast<unsigned>(o)) red[threadIdx.x] += red[threadIdx.x + o];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) grad_lam[blockIdx.x] = static_cast<float>(-red[0]);
-}
-
 // ---------------------------------------------------------------------- sums
 
 // Edges in the order of their sources: the row each came to and its weights
 // and logit gradients as planes, so that every slice of the sums below reads
 // them in sequence.  One wave per 64 edges; a lane reads its edge's rows.
+// The last H blocks sum the gradient of lam instead: -sum_d t1[d][h], in a
+// fixed order.
 template <bool V4>
 __global__ void __launch_bounds__(kThreads) regroup_kernel(const int *__restrict__ perm, const int *__restrict__ src_ptr,
                                                            int n_src, int E, int H, const int *__restrict__ dst,
                                                            const float *__restrict__ wr, const float *__restrict__ dl,
                                                            int64_t ldw, int *__restrict__ dst_out,
-                                                           float *__restrict__ w_out, float *__restrict__ dl_out) {
+                                                           float *__restrict__ w_out, float *__restrict__ dl_out,
+                                                           const float *__restrict__ t1, int n_dst,
+                                                           float *__restrict__ grad_lam) {
+  if (blockIdx.x + H >= gridDim.x) {
+    __shared__ double red[kThreads];
+    const int h = blockIdx.x + H - gridDim.x;
+    double sum = 0.0;
+    for (int d0 = threadIdx.x; d0 < n_dst; d0 += 16 * kThreads) {
+      float v[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) v[u] = t1[static_cast<int64_t>(min(d0 + u * kThreads, n_dst - 1)) * H + h];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) sum += d0 + u * kThreads < n_dst ? v[u] : 0.0f;
+    }
+    red[threadIdx.x] = sum;
+    __syncthreads();
+    for (int o = kThreads / 2; o > 0; o >>= 1) {
+      if (threadIdx.x < static_cast<unsigned>(o)) red[threadIdx.x] += red[threadIdx.x + o];
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) grad_lam[h] = static_cast<float>(-red[0]);
+    return;
+  }
   const int j = blockIdx.x * kThreads + threadIdx.x;
   if (j >= min(max(src_ptr[n_src], 0), E)) return;
   const int e = perm[j];
@@ -853,6 +859,7 @@ struct SumArgs {
   int H, C, Ch, width;  // out row = width elements; column c of width has head (c % C) / Ch
   int S, SV, EPW;       // slices, vectors a slice, edges a wave takes at once
   int BE;               // edges staged at a time, a multiple of what a wave takes in flight
+  int planes;           // heads a slice meets: all, or where a row is one component those of its columns
   int unit0, units, blocks;  // first unit of the launch; rows + pieces; blocks a slice in the launch
   float scale;
   float *part;          // [pieces][width]
@@ -875,7 +882,7 @@ template <int NR, bool NARROW> struct Batch {
   float w[NR];
 
   // Edges past the end and rows outside X have weight 0 and row 0.
-  __device__ inline void fetch(const SumArgs &a, int j0, int e, int lane) {
+  __device__ inline void fetch(const SumArgs &a, const float *planes, int n_planes, int j0, int e, int lane) {
     x = -1;
     if (lane < a.BE && j0 + lane < e) x = a.col[j0 + lane];
     const bool live = static_cast<unsigned>(x) < static_cast<unsigned>(a.n_x);
@@ -888,11 +895,11 @@ template <int NR, bool NARROW> struct Batch {
       if ((there >> i) & 1)
 #pragma unroll
         for (int t = 0; t < NR; ++t)
-          w[t] = a.w[min(4 * t + h0, a.H - 1) * a.ldw + j0 + i];
+          w[t] = planes[min(4 * t + h0, n_planes - 1) * a.ldw + j0 + i];
     } else if (live) {
       // plane t's address is the wave's; planes past the last are read again and not used
 #pragma unroll
-      for (int t = 0; t < NR; ++t) w[t] = (a.w + min(t, a.H - 1) * a.ldw + j0)[static_cast<uint32_t>(lane)];
+      for (int t = 0; t < NR; ++t) w[t] = (planes + min(t, n_planes - 1) * a.ldw + j0)[static_cast<uint32_t>(lane)];
     }
   }
 
@@ -913,22 +920,22 @@ enum { kScalar, kOffset, kLong };
 // cost as much as others).  SAFE skips weights of 0, so that what such a row
 // of X holds stays out.
 template <typename TX, int VW, int MODE, int NR, bool NARROW, bool SAFE>
-__device__ inline void gather_rows(const SumArgs &a, const TX *X, int b, int e, int c, int head, int grp, bool on,
-                                   int lane, float *sw, uint32_t *sx, float (&acc)[VW]) {
+__device__ inline void gather_rows(const SumArgs &a, const TX *X, const float *planes, int n_planes, int b, int e, int c, int head,
+                                   int grp, bool on, int lane, float *sw, uint32_t *sx, float (&acc)[VW]) {
   constexpr int U = MODE == kScalar ? 8 : 4;  // edges a group has in flight
   const int step = MODE == kScalar ? U : a.EPW * U;
   const uint32_t pitch = static_cast<uint32_t>(a.ldx * sizeof(TX));
   using B = Batch<NR, NARROW>;
   const float *swh = sw + head * B::kPitch;
   B next;
-  next.fetch(a, b, e, lane);
+  next.fetch(a, planes, n_planes, b, e, lane);
   for (int j0 = b; j0 < e; j0 += a.BE) {
     next.stage(lane, sw);
     const int x = next.x;
     if constexpr (MODE == kOffset) sx[lane] = static_cast<uint32_t>(x) * pitch;
     if constexpr (MODE == kLong) sx[lane] = x;
     wave_lds_order();
-    if (j0 + a.BE < e) next.fetch(a, j0 + a.BE, e, lane);  // under way while this batch is summed
+    if (j0 + a.BE < e) next.fetch(a, planes, n_planes, j0 + a.BE, e, lane);  // under way while this batch is summed
     const int n = min(a.BE, e - j0);
     for (int i0 = 0; i0 < n; i0 += step) {
       const int i = MODE == kScalar ? i0 : i0 + grp * U;
@@ -1010,11 +1017,15 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const T
   const int vj = slice * a.SV + gl;
   const bool on = gl < a.SV && grp < a.EPW && vj < nv;
   const int c = (on ? vj : nv - 1) * VW;
-  const int head = (c % a.C) / a.Ch;
+  // heads are counted from the first that the slice meets
+  const int first = a.width == a.C ? slice * a.SV * VW / a.Ch : 0;
+  const int head = (c % a.C) / a.Ch - first;
+  const float *planes = a.w + first * a.ldw;
+  const int n_planes = min(a.planes, a.H - first);
   float acc[VW];
 #pragma unroll
   for (int k = 0; k < VW; ++k) acc[k] = 0.0f;
-  gather_rows<TX, VW, MODE, NR, NARROW, false>(a, X, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
+  gather_rows<TX, VW, MODE, NR, NARROW, false>(a, X, planes, n_planes, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
   // A sum that is finite had no infinity or NaN in it, so its weights of 0
   // added 0.  One that is not is taken again with those edges left out.
   bool odd = false;
@@ -1023,7 +1034,7 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const T
   if (__any(odd)) {
 #pragma unroll
     for (int k = 0; k < VW; ++k) acc[k] = 0.0f;
-    gather_rows<TX, VW, MODE, NR, NARROW, true>(a, X, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
+    gather_rows<TX, VW, MODE, NR, NARROW, true>(a, X, planes, n_planes, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
   }
   if constexpr (MODE != kScalar) {
     float sum[VW];
@@ -1133,7 +1144,7 @@ egnn_status make_shape_of(const egnn_attn_desc *d, const egnn_graph *g, Shape *s
   s->E = static_cast<int>(g->n_edges);
   const int fit = 4096 / (2 * s->H);  // 16 KB of logits
   s->T = fit < 64 ? 64 : fit > 512 ? 512 : fit;
-  s->TP = piece_edges(static_cast<int64_t>(s->n_dst) * kWaves, s->n_dst, s->E, s->T);
+  s->TP = piece_edges(static_cast<int64_t>(s->n_dst) * kWaves, s->n_dst, s->E, 64);
   s->pieces = s->E > s->TP ? 2 * ((static_cast<int64_t>(s->E) + s->TP - 1) / s->TP) : 0;
   return EGNN_OK;
 }
@@ -1148,6 +1159,8 @@ struct SumPlan {
 SumPlan sum_plan(int n_rows, int n_x, int E, int nv, int bytes) {
   SumPlan p;
   if (nv <= kWave) {
+    // one slice, whatever X is: eight of a line each took 103 us where one takes
+    // 81 (rows of 1 KB, 8 MB of them, 1.1 M edges)
     p.S = 1;
     p.SV = nv;
   } else {
@@ -1258,8 +1271,16 @@ egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream
   a.SV = p.SV;
   a.EPW = p.EPW;
   a.T = p.T;
+  a.planes = a.H;
+  if (a.width == a.C && a.S > 1) {
+    a.planes = 1;
+    for (int i = 0; i < a.S; ++i) {
+      const int c0 = i * a.SV * vw, c1 = (i + 1) * a.SV * vw < a.width ? (i + 1) * a.SV * vw : a.width;
+      if (c0 < c1 && (c1 - 1) / a.Ch - c0 / a.Ch + 1 > a.planes) a.planes = (c1 - 1) / a.Ch - c0 / a.Ch + 1;
+    }
+  }
   // whole rounds of the edges in flight
-  const int round = p.EPW == 1 ? 8 : 4 * p.EPW, stage = a.H <= 16 ? kWave : 16;
+  const int round = p.EPW == 1 ? 8 : 4 * p.EPW, stage = a.planes <= 16 ? kWave : 16;
   if (round > stage) a.EPW = stage / 4;
   a.BE = stage / (a.EPW == 1 ? 8 : 4 * a.EPW) * (a.EPW == 1 ? 8 : 4 * a.EPW);
   const int mode = a.EPW == 1                                                                       ? kScalar
@@ -1277,10 +1298,10 @@ egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream
     const unsigned grid = static_cast<unsigned>(a.blocks) * a.S;
     // registers for the next edges' weights: as few as the heads allow
     constexpr int V = 16 / sizeof(TX);
-    if (vw > 1 && a.H <= 8) launch_sum<TX, TO, V, 8, false>(grid, mode, st, a, X, out);
-    else if (vw > 1 && a.H <= 16) launch_sum<TX, TO, V, 16, false>(grid, mode, st, a, X, out);
+    if (vw > 1 && a.planes <= 8) launch_sum<TX, TO, V, 8, false>(grid, mode, st, a, X, out);
+    else if (vw > 1 && a.planes <= 16) launch_sum<TX, TO, V, 16, false>(grid, mode, st, a, X, out);
     else if (vw > 1) launch_sum<TX, TO, V, 16, true>(grid, mode, st, a, X, out);
-    else if (a.H <= 16) launch_sum<TX, TO, 1, 16, false>(grid, mode, st, a, X, out);
+    else if (a.planes <= 16) launch_sum<TX, TO, 1, 16, false>(grid, mode, st, a, X, out);
     else launch_sum<TX, TO, 1, 16, true>(grid, mode, st, a, X, out);
     EGNN_CHECK_LAUNCH();
   }
@@ -1476,19 +1497,11 @@ egnn_status backward(const Shape &s, const egnn_graph *g, const T *q, const T *k
     }
   }
   {
-    Timed t(st, "attn_lam_grad", 0.0, 4.0 * s.n_dst * s.H);
-    lam_grad_kernel<<<s.H, 1024, 0, st>>>(t1, s.n_dst, s.H, glam);
-    EGNN_CHECK_LAUNCH();
-  }
-  if (s.E > 0) {
     Timed t(st, "attn_regroup", 0.0, static_cast<double>(s.E) * (24.0 * s.H + 12));
-    const unsigned grid = ceil_div(s.E, kThreads);
-    if (s.H % 4 == 0 && aligned16(dl))
-      regroup_kernel<true><<<grid, kThreads, 0, st>>>(g->src_perm, g->src_ptr, s.n_src, s.E, s.H, sv.dst, wr, dl,
-                                                      plane(s), dst_src, w_src, dlp_src);
-    else
-      regroup_kernel<false><<<grid, kThreads, 0, st>>>(g->src_perm, g->src_ptr, s.n_src, s.E, s.H, sv.dst, wr, dl,
-                                                       plane(s), dst_src, w_src, dlp_src);
+    const unsigned grid = ceil_div(s.E, kThreads) + s.H;
+    const auto kernel = s.H % 4 == 0 && aligned16(dl) ? regroup_kernel<true> : regroup_kernel<false>;
+    kernel<<<grid, kThreads, 0, st>>>(g->src_perm, g->src_ptr, s.n_src, s.E, s.H, sv.dst, wr, dl, plane(s), dst_src,
+                                      w_src, dlp_src, t1, s.n_dst, glam);
     EGNN_CHECK_LAUNCH();
   }
   SumArgs m{};

@@ -448,11 +448,11 @@ struct LogitArgs {
   float2 *piece_stats;            // [pieces][2H]
 };
 
-// Edge weights of [b, b + cnt) from their logits (in LDS, or in a.maps).
-__device__ inline void edge_weights(const LogitArgs &a, const float2 *lg, const float2 *fin, int b, int cnt) {
+// Edge weights of [b, b + cnt) whose logits are in a.maps.
+__device__ inline void edge_weights(const LogitArgs &a, const float2 *fin, int b, int cnt) {
   float2 *maps = a.maps + static_cast<int64_t>(b) * a.H;
   for_decisions(b, cnt, a.H, a.drop, [&](int at, int i, int h, float m) {
-    const float2 l = lg[at];
+    const float2 l = maps[at];
     const float2 al = make_float2(weight_of(l.x, fin[2 * h]), weight_of(l.y, fin[2 * h + 1]));
     if (a.keep) maps[at] = al;
     a.w[h * a.ldw + b + i] = m == 0.0f ? 0.0f : m * (al.x - a.lam[h] * al.y);
@@ -464,11 +464,13 @@ __device__ inline void edge_weights(const LogitArgs &a, const float2 *lg, const 
 template <typename T, int VW, int NIT, bool ONE>
 __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *__restrict__ q,
                                                           const T *__restrict__ k) {
-  extern __shared__ __align__(16) float lg[];  // [T][2H], then the sources [T]
-  int *scol = reinterpret_cast<int *>(lg + a.T * 2 * a.H);
+  extern __shared__ float lg[];  // [T][2H + 1], then the sources [T]
+  int *scol = reinterpret_cast<int *>(lg + a.T * (2 * a.H + 1));
   __shared__ float red[kWaves][kWave];
   __shared__ float2 fin[kWave];
-  const int H2 = 2 * a.H;
+  __shared__ float slam[kMaxHeads];
+  const int H2 = 2 * a.H, pitch = H2 + 1;
+  if (threadIdx.x < static_cast<unsigned>(a.H)) slam[threadIdx.x] = a.lam[threadIdx.x];
   int d, b, e;
   const int p = static_cast<int>(blockIdx.x) - a.n_dst;
   if (p < 0) {
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *
     edge_dots<T, T, VW, NIT, ONE>(q + static_cast<int64_t>(d) * a.ldq, k, a.ldk, scol,
                                   uniform(threadIdx.x >> 6) * step, kWaves * step, cnt, 1, H2, H2 * a.D, a.team,
                                   [&](int i, int h, float x, bool first) {
-                                    lg[i * H2 + h] = first ? x : lg[i * H2 + h] + x;
+                                    lg[i * pitch + h] = first ? x : lg[i * pitch + h] + x;
                                   });
     __syncthreads();
     float Mc = -INFINITY;
@@ -516,9 +518,9 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *
         for (int u = 0; u < 4; ++u) {
           const int i = i0 + u * R;
           if (i >= cnt) break;
-          float l = lg[i * H2 + col] * a.scale + bv[u];
+          float l = lg[i * pitch + col] * a.scale + bv[u];
           if (bv[u] == -INFINITY || scol[i] < 0) l = -INFINITY;  // masked, whatever the product is
-          lg[i * H2 + col] = l;
+          lg[i * pitch + col] = l;
           if (!whole) reinterpret_cast<float *>(a.maps)[o + i * H2] = l;
           Mc = fmaxf(Mc, l);
         }
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *
     const float Mn = fmaxf(M, column_reduce(Mc, Hp, red, MaxOp()));
     float Sc = 0.0f;
     if (col < H2 && Mn != -INFINITY)
-      for (int i = r0; i < cnt; i += R) Sc += __expf(lg[i * H2 + col] - Mn);
+      for (int i = r0; i < cnt; i += R) Sc += __expf(lg[i * pitch + col] - Mn);
     S = (M == -INFINITY ? 0.0f : S * __expf(M - Mn)) + column_reduce(Sc, Hp, red, SumOp());
     M = Mn;
   }
@@ -534,10 +536,41 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *
     if (r0 == 0 && col < H2) a.piece_stats[static_cast<int64_t>(p) * H2 + col] = make_float2(M, S);
     return;
   }
-  if (r0 == 0 && col < H2) fin[col] = finish_stats(M, S);
-  __syncthreads();  // orders the logits that this block wrote to memory, too
-  edge_weights(a, whole ? reinterpret_cast<const float2 *>(lg) : a.maps + static_cast<int64_t>(b) * a.H, fin, b,
-               e - b);
+  const float2 st = finish_stats(M, S);
+  if (!whole) {
+    if (r0 == 0 && col < H2) fin[col] = st;
+    __syncthreads();  // orders the logits that this block wrote to memory, too
+    edge_weights(a, fin, b, e - b);
+    return;
+  }
+  const int cnt = e - b;
+  if (col < H2)
+    for (int i = r0; i < cnt; i += R) {
+      const float al = weight_of(lg[i * pitch + col], st);
+      lg[i * pitch + col] = al;
+      if (a.keep) reinterpret_cast<float *>(a.maps)[static_cast<int64_t>(b + i) * H2 + col] = al;
+    }
+  __syncthreads();
+  // A thread writes its edge's heads, so that a wave's lanes write neighbouring
+  // edges of a plane, and draws eight decisions at a time.
+  DropKey key{};
+  if (a.drop.t != 0) key = drop_key(a.drop);
+  for (int i = threadIdx.x; i < cnt; i += kThreads) {
+    const int64_t at = static_cast<int64_t>(b + i) * a.H;
+    // heads of one draw group after another; the groups start at multiples of 8 of at + h
+    for (int h0 = -static_cast<int>(at & 7); h0 < a.H; h0 += 8) {
+      uint4 draws = make_uint4(0, 0, 0, 0);
+      if (a.drop.t != 0) draws = philox4x32(static_cast<uint64_t>((at + h0) >> 3), key);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int h = h0 + u;
+        if (h < 0 || h >= a.H) continue;
+        float w = lg[i * pitch + 2 * h] - slam[h] * lg[i * pitch + 2 * h + 1];
+        if (a.drop.t != 0) w = drop_draw(draws, u) >= a.drop.t ? w * a.drop.factor : 0.0f;
+        a.w[h * a.ldw + b + i] = w;
+      }
+    }
+  }
 }
 
 // Long rows: the pieces' statistics joined, then their edge weights.
@@ -565,7 +598,7 @@ __global__ void __launch_bounds__(kThreads) long_weights_kernel(LogitArgs a) {
   S = column_reduce(S, Hp, red, SumOp());
   if (r0 == 0 && col < H2) fin[col] = finish_stats(M, S);
   __syncthreads();
-  edge_weights(a, a.maps + static_cast<int64_t>(pc.begin) * a.H, fin, pc.begin, pc.end - pc.begin);
+  edge_weights(a, fin, pc.begin, pc.end - pc.begin);
 }
 
 struct DotArgs {
@@ -1369,7 +1402,7 @@ egnn_status forward(const Shape &s, const egnn_graph *g, const T *q, const T *k,
     a.team = make_team(1, 2 * s.H, vec ? s.D / V : s.D);
     a.Hpl = log2_ceil(2 * s.H);
     const unsigned grid = static_cast<unsigned>(s.n_dst + s.pieces);
-    const size_t lds = static_cast<size_t>(s.T) * (2 * s.H + 1) * 4;
+    const size_t lds = static_cast<size_t>(s.T) * (2 * s.H + 2) * 4;
     {
       Timed t(st, "attn_logits", 4.0 * s.E * s.H * s.D,
               static_cast<double>(s.E) * (12.0 * s.H + 8 + (bias ? 8.0 * s.H : 0)) +

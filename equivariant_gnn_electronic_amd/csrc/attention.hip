@@ -684,7 +684,8 @@ struct GradArgs {
 
 // The logits' gradients of edges [c0, c0 + cnt), whose weights lie in al
 // (pitch 2H + 1) and u in us: rows first, then through al into planes.
-__device__ inline void logit_grads(const GradArgs &a, int c0, int cnt, const float2 *tt, float *al, const float *us) {
+__device__ inline void logit_grads(const GradArgs &a, int c0, int cnt, const float2 *tt, const float *slam, float *al,
+                                   const float *us) {
   const int H = a.H, pitch = 2 * H + 1;
   float2 *dl = a.dl + static_cast<int64_t>(c0) * H;
   for (int f = threadIdx.x; f < cnt * H; f += kThreads) {
@@ -693,7 +694,7 @@ __device__ inline void logit_grads(const GradArgs &a, int c0, int cnt, const flo
     const float u = us[f];
     // a weight of exactly 0 (masked) has no gradient, whatever the row of v holds
     const float2 g = make_float2(w[0] == 0.0f ? 0.0f : w[0] * (u - tt[h].x),
-                                 w[1] == 0.0f ? 0.0f : -a.lam[h] * w[1] * (u - tt[h].y));
+                                 w[1] == 0.0f ? 0.0f : -slam[h] * w[1] * (u - tt[h].y));
     dl[f] = g;
     w[0] = g.x;
     w[1] = g.y;
@@ -717,24 +718,28 @@ __device__ inline void load_maps(const GradArgs &a, int c0, int cnt, float *al) 
 
 // Rows and pieces of more than T edges: their gradients once the row's sums
 // are known.
-__device__ inline void logit_grads_again(const GradArgs &a, int b, int e, const float2 *tt, float *al, float *us) {
+__device__ inline void logit_grads_again(const GradArgs &a, int b, int e, const float2 *tt, const float *slam, float *al,
+                                         float *us) {
   for (int c0 = b; c0 < e; c0 += a.T) {
     const int cnt = min(a.T, e - c0);
     __syncthreads();
     load_maps(a, c0, cnt, al);
     for (int f = threadIdx.x; f < cnt * a.H; f += kThreads) us[f] = a.u[static_cast<int64_t>(c0) * a.H + f];
     __syncthreads();
-    logit_grads(a, c0, cnt, tt, al, us);
+    logit_grads(a, c0, cnt, tt, slam, al, us);
   }
 }
 
 // One block per row (or piece): the softmax's backward for both maps, T edges
 // at a time.
 __global__ void __launch_bounds__(kThreads) logit_grad_kernel(GradArgs a) {
-  extern __shared__ float al[];  // [T][2H + 1], then u [T][H]
+  extern __shared__ float al[];  // [T][2H + 1], then u [T][H] and the decisions [T][H]
   float *us = al + a.T * (2 * a.H + 1);
+  uint8_t *kept = reinterpret_cast<uint8_t *>(us + a.T * a.H);
   __shared__ float red[kWaves][kWave];
   __shared__ float2 tt[kMaxHeads];
+  __shared__ float slam[kMaxHeads];
+  if (threadIdx.x < static_cast<unsigned>(a.H)) slam[threadIdx.x] = a.lam[threadIdx.x];
   int d, b, e;
   const int p = static_cast<int>(blockIdx.x) - a.n_dst;
   if (p < 0) {
@@ -762,13 +767,19 @@ __global__ void __launch_bounds__(kThreads) logit_grad_kernel(GradArgs a) {
     __syncthreads();
     load_maps(a, c0, cnt, al);
     __syncthreads();
-    for_decisions(c0, cnt, H, a.drop, [&](int at, int i, int hd, float m) {
+    if (a.drop.t != 0) {
+      for_decisions(c0, cnt, H, a.drop, [&](int at, int, int, float m) { kept[at] = m != 0.0f; });
+      __syncthreads();
+    }
+    for (int f = threadIdx.x; f < cnt * H; f += kThreads) {
+      const int i = f / H, hd = f - i * H;
       const float *w = al + i * pitch + 2 * hd;
-      a.wr[o0 + at] = m == 0.0f ? 0.0f : m * (w[0] - a.lam[hd] * w[1]);
-      const float x = m == 0.0f ? 0.0f : m * a.u[o0 + at];
-      us[at] = x;
-      if (again) a.u[o0 + at] = x;
-    });
+      const bool on = a.drop.t == 0 || kept[f] != 0;
+      a.wr[o0 + f] = on ? a.drop.factor * (w[0] - slam[hd] * w[1]) : 0.0f;
+      const float x = on ? a.drop.factor * a.u[o0 + f] : 0.0f;
+      us[f] = x;
+      if (again) a.u[o0 + f] = x;
+    }
     __syncthreads();
     if (h < H)
       for (int i = r0; i < cnt; i += R) {
@@ -788,8 +799,8 @@ __global__ void __launch_bounds__(kThreads) logit_grad_kernel(GradArgs a) {
     a.t1[static_cast<int64_t>(d) * H + h] = t1;
   }
   __syncthreads();
-  if (again) logit_grads_again(a, b, e, tt, al, us);
-  else logit_grads(a, b, e - b, tt, al, us);
+  if (again) logit_grads_again(a, b, e, tt, slam, al, us);
+  else logit_grads(a, b, e - b, tt, slam, al, us);
 }
 
 // Long rows: the pieces' sums joined, then the logits' gradients.
@@ -798,6 +809,8 @@ __global__ void __launch_bounds__(kThreads) long_grad_kernel(GradArgs a) {
   float *us = al + a.T * (2 * a.H + 1);
   __shared__ float red[kWaves][kWave];
   __shared__ float2 tt[kMaxHeads];
+  __shared__ float slam[kMaxHeads];
+  if (threadIdx.x < static_cast<unsigned>(a.H)) slam[threadIdx.x] = a.lam[threadIdx.x];
   const Piece pc = find_piece(blockIdx.x, a.TP, a.row_ptr, a.n_dst, a.E, [&](int pos) { return a.dst[pos]; });
   if (pc.row < 0) return;
   int b, e;
@@ -819,7 +832,7 @@ __global__ void __launch_bounds__(kThreads) long_grad_kernel(GradArgs a) {
     if (pc.begin == b) a.t1[static_cast<int64_t>(pc.row) * H + h] = t1;
   }
   __syncthreads();
-  logit_grads_again(a, pc.begin, pc.end, tt, al, us);
+  logit_grads_again(a, pc.begin, pc.end, tt, slam, al, us);
 }
 
 // ---------------------------------------------------------------------- sums
@@ -1517,7 +1530,7 @@ egnn_status backward(const Shape &s, const egnn_graph *g, const T *q, const T *k
     a.t1 = t1;
     a.u = u;
     a.piece_t = piece_t;
-    const size_t lds = static_cast<size_t>(s.T) * (3 * s.H + 1) * 4;
+    const size_t lds = static_cast<size_t>(s.T) * ((3 * s.H + 1) * 4 + s.H);
     {
       Timed t(st, "attn_logit_grad", 0.0, static_cast<double>(s.E) * 36.0 * s.H);
       logit_grad_kernel<<<static_cast<unsigned>(s.n_dst + s.pieces), kThreads, lds, st>>>(a);

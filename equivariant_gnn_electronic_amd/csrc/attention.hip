@@ -20,6 +20,7 @@
 // (piece 2x: the row that owns edge xT) and the start of another (piece 2x+1:
 // the row that owns the window's last edge, if it starts inside the window).
 // Pieces are joined by a later launch, in edge order.
+#include <algorithm>
 #include <cmath>
 
 #include "common.h"
@@ -52,6 +53,19 @@ template <> struct Vec<float, 1> {
 template <> struct Vec<uint16_t, 1> {
   __device__ static inline void ld(const uint16_t *p, float (&v)[1]) { v[0] = bf16_to_f32(*p); }
   __device__ static inline void st(uint16_t *p, const float (&v)[1]) { *p = f32_to_bf16(v[0]); }
+};
+template <> struct Vec<float, 2> {
+  __device__ static inline void ld(const float *p, float (&v)[2]) {
+    const float2 a = *reinterpret_cast<const float2 *>(p);
+    v[0] = a.x; v[1] = a.y;
+  }
+};
+template <> struct Vec<uint16_t, 4> {
+  __device__ static inline void ld(const uint16_t *p, float (&v)[4]) {
+    const uint2 a = *reinterpret_cast<const uint2 *>(p);
+    v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xFFFF0000u);
+  }
 };
 template <> struct Vec<float, 4> {
   __device__ static inline void ld(const float *p, float (&v)[4]) {
@@ -101,7 +115,7 @@ __device__ inline uint64_t scalar(uint64_t v) {
   return v;
 }
 
-// One vector as it lies in memory (16 bytes, or one element), so that loads can
+// One vector as it lies in memory (16 or 8 bytes, or one element), so that loads can
 // be issued apart from the conversion; zero bits are zeros in either type.
 template <typename T, int VW> struct Raw;
 template <> struct Raw<float, 4> {
@@ -119,6 +133,19 @@ template <> struct Raw<uint16_t, 8> {
       v[2 * i] = __uint_as_float(w[i] << 16);
       v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
+  }
+};
+template <> struct Raw<float, 2> {
+  float2 r = make_float2(0.0f, 0.0f);
+  __device__ inline void ld(const float *p) { r = *reinterpret_cast<const float2 *>(p); }
+  __device__ inline void get(float (&v)[2]) const { v[0] = r.x; v[1] = r.y; }
+};
+template <> struct Raw<uint16_t, 4> {
+  uint2 r = make_uint2(0, 0);
+  __device__ inline void ld(const uint16_t *p) { r = *reinterpret_cast<const uint2 *>(p); }
+  __device__ inline void get(float (&v)[4]) const {
+    v[0] = __uint_as_float(r.x << 16); v[1] = __uint_as_float(r.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(r.y << 16); v[3] = __uint_as_float(r.y & 0xFFFF0000u);
   }
 };
 template <typename T> struct Raw<T, 1> {
@@ -965,14 +992,17 @@ enum { kScalar, kOffset, kLong };
 // nothing (a lookup of the vector cache serves four lanes: idle ones would
 // cost as much as others).  SAFE skips weights of 0, so that what such a row
 // of X holds stays out.
-template <typename TX, int VW, int MODE, int NR, bool NARROW, bool SAFE>
-__device__ inline void gather_rows(const SumArgs &a, const TX *X, const float *planes, int n_planes, int b, int e, int c, int head,
-                                   int grp, bool on, int lane, float *sw, uint32_t *sx, float (&acc)[VW]) {
+template <typename TX, int VW, int MODE, int NR, bool NARROW, bool MIX, bool SAFE>
+__device__ inline void gather_rows(const SumArgs &a, const TX *X, const float *planes, int n_planes, int b, int e, int c,
+                                   const int (&head)[VW], int grp, bool on, int lane, float *sw, uint32_t *sx, float (&acc)[VW]) {
   constexpr int U = MODE == kScalar ? 8 : 4;  // edges a group has in flight
   const int step = MODE == kScalar ? U : a.EPW * U;
   const uint32_t pitch = static_cast<uint32_t>(a.ldx * sizeof(TX));
   using B = Batch<NR, NARROW>;
-  const float *swh = sw + head * B::kPitch;
+  constexpr int NH = MIX ? VW : 1;  // heads of a vector
+  const float *swh[NH];
+#pragma unroll
+  for (int k = 0; k < NH; ++k) swh[k] = sw + head[k] * B::kPitch;
   B next;
   next.fetch(a, planes, n_planes, b, e, lane);
   for (int j0 = b; j0 < e; j0 += a.BE) {
@@ -1009,21 +1039,26 @@ __device__ inline void gather_rows(const SumArgs &a, const TX *X, const float *p
             base += static_cast<uint64_t>(rows[u & 3]) * pitch;
           v[u].ld(reinterpret_cast<const TX *>(base + at));
         }
-        float w[U];
+        float w[U][NH];
 #pragma unroll
-        for (int u = 0; u < U; u += 4) {
-          const float4 f = *reinterpret_cast<const float4 *>(swh + i + u);
-          w[u] = f.x;
-          w[u + 1] = f.y;
-          w[u + 2] = f.z;
-          w[u + 3] = f.w;
-        }
+        for (int k = 0; k < NH; ++k)
+#pragma unroll
+          for (int u = 0; u < U; u += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(swh[k] + i + u);
+            w[u][k] = f.x;
+            w[u + 1][k] = f.y;
+            w[u + 2][k] = f.z;
+            w[u + 3][k] = f.w;
+          }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           float r[VW];
           v[u].get(r);
 #pragma unroll
-          for (int k = 0; k < VW; ++k) acc[k] = fmaf(w[u], SAFE && w[u] == 0.0f ? 0.0f : r[k], acc[k]);
+          for (int k = 0; k < VW; ++k) {
+            const float wk = w[u][MIX ? k : 0];
+            acc[k] = fmaf(wk, SAFE && wk == 0.0f ? 0.0f : r[k], acc[k]);
+          }
         }
       }
     }
@@ -1033,7 +1068,7 @@ __device__ inline void gather_rows(const SumArgs &a, const TX *X, const float *p
 
 // out[r] = scale sum over the row's edges of w[e][head] X[col[e]].  One wave
 // per (row or piece, slice of columns).
-template <typename TX, typename TO, int VW, int MODE, int NR, bool NARROW>
+template <typename TX, typename TO, int VW, int MODE, int NR, bool NARROW, bool MIX>
 __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const TX *__restrict__ X,
                                                               TO *__restrict__ out) {
   __shared__ __align__(16) float sw[kWaves][Batch<NR, NARROW>::kFloats];
@@ -1065,13 +1100,15 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const T
   const int c = (on ? vj : nv - 1) * VW;
   // heads are counted from the first that the slice meets
   const int first = a.width == a.C ? slice * a.SV * VW / a.Ch : 0;
-  const int head = (c % a.C) / a.Ch - first;
+  int head[VW];
+#pragma unroll
+  for (int k = 0; k < VW; ++k) head[k] = ((c + k) % a.C) / a.Ch - first;
   const float *planes = a.w + first * a.ldw;
   const int n_planes = min(a.planes, a.H - first);
   float acc[VW];
 #pragma unroll
   for (int k = 0; k < VW; ++k) acc[k] = 0.0f;
-  gather_rows<TX, VW, MODE, NR, NARROW, false>(a, X, planes, n_planes, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
+  gather_rows<TX, VW, MODE, NR, NARROW, MIX, false>(a, X, planes, n_planes, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
   // A sum that is finite had no infinity or NaN in it, so its weights of 0
   // added 0.  One that is not is taken again with those edges left out.
   bool odd = false;
@@ -1080,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const T
   if (__any(odd)) {
 #pragma unroll
     for (int k = 0; k < VW; ++k) acc[k] = 0.0f;
-    gather_rows<TX, VW, MODE, NR, NARROW, true>(a, X, planes, n_planes, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
+    gather_rows<TX, VW, MODE, NR, NARROW, MIX, true>(a, X, planes, n_planes, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
   }
   if constexpr (MODE != kScalar) {
     float sum[VW];
@@ -1244,11 +1281,12 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Vector width: 16-byte vectors that lie in one head and one row; else single
-// elements (any width, stride and alignment).
+// Elements of the widest load (16 or 8 bytes, or one element) that lies in one
+// head and one row and is aligned.
 template <typename T> int vec_width(int Ch, int64_t ld, const void *p) {
-  constexpr int V = 16 / sizeof(T);
-  return Ch % V == 0 && ld % V == 0 && aligned16(p) ? V : 1;
+  for (int V = 16 / sizeof(T); V * sizeof(T) >= 8; V /= 2)
+    if (Ch % V == 0 && ld % V == 0 && reinterpret_cast<uintptr_t>(p) % (V * sizeof(T)) == 0) return V;
+  return 1;
 }
 
 struct Saved {
@@ -1301,17 +1339,21 @@ size_t ws_bwd_of(const Shape &s) {
          align256(static_cast<size_t>(s.pieces) * H * 8) + part;
 }
 
-template <typename TX, typename TO, int VW, int NR, bool NARROW>
+template <typename TX, typename TO, int VW, int NR, bool NARROW, bool MIX>
 void launch_sum(unsigned grid, int mode, hipStream_t st, const SumArgs &a, const TX *X, TO *out) {
-  if (mode == kScalar) gather_sum_kernel<TX, TO, VW, kScalar, NR, NARROW><<<grid, kThreads, 0, st>>>(a, X, out);
-  else if (mode == kOffset) gather_sum_kernel<TX, TO, VW, kOffset, NR, NARROW><<<grid, kThreads, 0, st>>>(a, X, out);
-  else gather_sum_kernel<TX, TO, VW, kLong, NR, NARROW><<<grid, kThreads, 0, st>>>(a, X, out);
+  if (mode == kScalar) gather_sum_kernel<TX, TO, VW, kScalar, NR, NARROW, MIX><<<grid, kThreads, 0, st>>>(a, X, out);
+  else if (mode == kOffset)
+    gather_sum_kernel<TX, TO, VW, kOffset, NR, NARROW, MIX><<<grid, kThreads, 0, st>>>(a, X, out);
+  else gather_sum_kernel<TX, TO, VW, kLong, NR, NARROW, MIX><<<grid, kThreads, 0, st>>>(a, X, out);
 }
 
 template <typename TX, typename TO>
 egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream_t st) {
   if (a.n_rows == 0) return EGNN_OK;
-  const int vw = vec_width<TX>(a.Ch, a.ldx, X) > 1 && aligned16(out) ? 16 / sizeof(TX) : 1;
+  // 16-byte vectors of a row; one may hold elements of several heads (mix)
+  constexpr int V = 16 / sizeof(TX);
+  const int vw = a.width % V == 0 && a.ldx % V == 0 && aligned16(X) && aligned16(out) ? V : 1;
+  const bool mix = vw > 1 && a.Ch % V != 0;
   const SumPlan p = sum_plan(a.n_rows, a.n_x, a.E, a.width / vw, vw * static_cast<int>(sizeof(TX)));
   a.S = p.S;
   a.SV = p.SV;
@@ -1322,7 +1364,7 @@ egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream
     a.planes = 1;
     for (int i = 0; i < a.S; ++i) {
       const int c0 = i * a.SV * vw, c1 = (i + 1) * a.SV * vw < a.width ? (i + 1) * a.SV * vw : a.width;
-      if (c0 < c1 && (c1 - 1) / a.Ch - c0 / a.Ch + 1 > a.planes) a.planes = (c1 - 1) / a.Ch - c0 / a.Ch + 1;
+      if (c0 < c1) a.planes = std::max(a.planes, (c1 - 1) / a.Ch - c0 / a.Ch + 1);
     }
   }
   // whole rounds of the edges in flight
@@ -1343,12 +1385,14 @@ egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream
     a.blocks = left < most ? left : most;
     const unsigned grid = static_cast<unsigned>(a.blocks) * a.S;
     // registers for the next edges' weights: as few as the heads allow
-    constexpr int V = 16 / sizeof(TX);
-    if (vw > 1 && a.planes <= 8) launch_sum<TX, TO, V, 8, false>(grid, mode, st, a, X, out);
-    else if (vw > 1 && a.planes <= 16) launch_sum<TX, TO, V, 16, false>(grid, mode, st, a, X, out);
-    else if (vw > 1) launch_sum<TX, TO, V, 16, true>(grid, mode, st, a, X, out);
-    else if (a.planes <= 16) launch_sum<TX, TO, 1, 16, false>(grid, mode, st, a, X, out);
-    else launch_sum<TX, TO, 1, 16, true>(grid, mode, st, a, X, out);
+    const bool narrow = a.planes > 16;
+    if (mix && !narrow) launch_sum<TX, TO, V, 16, false, true>(grid, mode, st, a, X, out);
+    else if (mix) launch_sum<TX, TO, V, 16, true, true>(grid, mode, st, a, X, out);
+    else if (vw > 1 && a.planes <= 8) launch_sum<TX, TO, V, 8, false, false>(grid, mode, st, a, X, out);
+    else if (vw > 1 && !narrow) launch_sum<TX, TO, V, 16, false, false>(grid, mode, st, a, X, out);
+    else if (vw > 1) launch_sum<TX, TO, V, 16, true, false>(grid, mode, st, a, X, out);
+    else if (!narrow) launch_sum<TX, TO, 1, 16, false, false>(grid, mode, st, a, X, out);
+    else launch_sum<TX, TO, 1, 16, true, false>(grid, mode, st, a, X, out);
     EGNN_CHECK_LAUNCH();
   }
   if (p.pieces) {
@@ -1411,8 +1455,8 @@ egnn_status forward(const Shape &s, const egnn_graph *g, const T *q, const T *k,
   a.piece_stats = piece_stats;
   if (s.E > 0) {
     constexpr int V = 16 / sizeof(T);
-    const bool vec = vec_width<T>(s.D, s.ldq, q) > 1 && vec_width<T>(s.D, s.ldk, k) > 1;
-    a.team = make_team(1, 2 * s.H, vec ? s.D / V : s.D);
+    const int vw = std::min(vec_width<T>(s.D, s.ldq, q), vec_width<T>(s.D, s.ldk, k));
+    a.team = make_team(1, 2 * s.H, s.D / vw);
     a.Hpl = log2_ceil(2 * s.H);
     const unsigned grid = static_cast<unsigned>(s.n_dst + s.pieces);
     const size_t lds = static_cast<size_t>(s.T) * (2 * s.H + 2) * 4;
@@ -1421,8 +1465,9 @@ egnn_status forward(const Shape &s, const egnn_graph *g, const T *q, const T *k,
               static_cast<double>(s.E) * (12.0 * s.H + 8 + (bias ? 8.0 * s.H : 0)) +
                   2.0 * s.H * s.D * sizeof(T) * (static_cast<double>(s.n_dst) + s.n_src));
       const bool one = a.team.esh == 6;
-      if (vec && one) launch_logits<T, V, true>(grid, lds, st, a, q, k);
-      else if (vec) launch_logits<T, V, false>(grid, lds, st, a, q, k);
+      if (vw == V && one) launch_logits<T, V, true>(grid, lds, st, a, q, k);
+      else if (vw == V) launch_logits<T, V, false>(grid, lds, st, a, q, k);
+      else if (vw > 1) launch_logits<T, V / 2, false>(grid, lds, st, a, q, k);
       else launch_logits<T, 1, false>(grid, lds, st, a, q, k);
       EGNN_CHECK_LAUNCH();
     }
@@ -1488,8 +1533,8 @@ egnn_status backward(const Shape &s, const egnn_graph *g, const T *q, const T *k
     a.K = s.K;
     a.ldv = s.ldv;
     a.u = u;
-    const bool vec = vec_width<T>(Ch, s.ldv, v) > 1 && aligned16(go);
-    a.team = make_team(s.K, s.H, vec ? Ch / V : Ch);
+    const int vw = std::min(vec_width<T>(Ch, s.ldv, v), aligned16(go) ? V : 1);
+    a.team = make_team(s.K, s.H, Ch / vw);
     a.parts = dot_parts(s, sizeof(T));
     a.T = piece_edges(static_cast<int64_t>(s.n_dst) * a.parts, s.n_dst, s.E, 128);
     const int64_t pieces = s.E > a.T ? 2 * ((static_cast<int64_t>(s.E) + a.T - 1) / a.T) : 0;
@@ -1504,8 +1549,10 @@ egnn_status backward(const Shape &s, const egnn_graph *g, const T *q, const T *k
       a.blocks = left < most ? left : most;
       const unsigned grid = static_cast<unsigned>(a.blocks) * a.parts;
       const bool one = a.team.esh == 6;
-      if (vec && one) launch_dots<T, V, true>(grid, st, a, go, v);
-      else if (vec) launch_dots<T, V, false>(grid, st, a, go, v);
+      if (vw == V && one) launch_dots<T, V, true>(grid, st, a, go, v);
+      else if (vw == V) launch_dots<T, V, false>(grid, st, a, go, v);
+      else if (vw > 1 && one) launch_dots<T, V / 2, true>(grid, st, a, go, v);
+      else if (vw > 1) launch_dots<T, V / 2, false>(grid, st, a, go, v);
       else launch_dots<T, 1, false>(grid, st, a, go, v);
       EGNN_CHECK_LAUNCH();
     }

@@ -41,6 +41,7 @@ constexpr int kMaxRows = kMaxBlocks / 2;
 constexpr int64_t kMaxStride = 1 << 29;    // a row's pitch in bytes is counted in 32 bits
 constexpr int64_t kSliceBytes = 3200000;   // of X in one XCD's L2
 constexpr int64_t kPartBytes = 3600000;    // of v in one XCD's L2 (dot products)
+constexpr int64_t kPairBytes = 8000000;    // of both X of two sums that share a launch
 constexpr int kMinSlice = 16;              // vectors of the narrowest slice
 
 // ------------------------------------------------------------------ helpers
@@ -265,8 +266,7 @@ __device__ inline void for_decisions(int b, int cnt, int H, const Drop &dr, F f)
 struct Slot {
   int slice, block;
 };
-__device__ inline Slot slot_of(int slices, int blocks) {
-  const int b = blockIdx.x;
+__device__ inline Slot slot_of(int slices, int blocks, int b) {
   if (slices <= 8) return Slot{b % slices, b / slices};
   return Slot{((b >> 3) / blocks) * 8 + (b & 7), (b >> 3) % blocks};
 }
@@ -376,7 +376,9 @@ __device__ inline void team_sum(float (&dot)[U], const Team &tm) {
 template <typename TA, typename TB, int VW, int NIT, bool ONE, typename Put>
 __device__ inline void edge_dots(const TA *arow, const TB *B, int64_t ldb, const int *scol, int i_first, int stride,
                                  int cnt, int K, int H, int C, const Team &tm, Put put) {
-  constexpr int U = NIT == 1 ? 8 : NIT == 2 ? 4 : NIT == 3 ? 3 : 2;  // 6 to 14 loads in flight
+  // edges in flight: 6 to 10 loads (two edges of 7 took 522 us where one takes
+  // 477: bf16 rows of 6.4 KB, 1.1 M edges; their registers cost a wave)
+  constexpr int U = NIT == 1 ? 8 : NIT == 2 ? 4 : NIT == 3 ? 3 : NIT <= 5 ? 2 : 1;
   const int lane = threadIdx.x & (kWave - 1);
   const int Ch = C / H, P = Ch / VW;
   const int es = ONE ? 0 : lane >> tm.esh;
@@ -648,7 +650,7 @@ template <typename T, int VW, int NIT, bool ONE>
 __global__ void __launch_bounds__(kThreads) value_dots_kernel(DotArgs a, const float *__restrict__ go,
                                                               const T *__restrict__ v) {
   __shared__ int scol[kWaves][kWave];
-  const Slot sl = slot_of(a.parts, a.blocks);
+  const Slot sl = slot_of(a.parts, a.blocks, blockIdx.x);
   const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x >> 6);
   const int unit = a.unit0 + sl.block * kWaves + wave;
   if (unit >= a.units) return;
@@ -1066,14 +1068,26 @@ __device__ inline void gather_rows(const SumArgs &a, const TX *X, const float *p
   }
 }
 
+// Two sums of one launch: blocks from `split` (a multiple of 8) on take the
+// second.
+template <typename TX, typename TO> struct SumPair {
+  SumArgs a[2];
+  const TX *X[2];
+  TO *out[2];
+  unsigned split;
+};
+
 // out[r] = scale sum over the row's edges of w[e][head] X[col[e]].  One wave
 // per (row or piece, slice of columns).
 template <typename TX, typename TO, int VW, int MODE, int NR, bool NARROW, bool MIX>
-__global__ void __launch_bounds__(kThreads) gather_sum_kernel(SumArgs a, const TX *__restrict__ X,
-                                                              TO *__restrict__ out) {
+__global__ void __launch_bounds__(kThreads) gather_sum_kernel(const SumPair<TX, TO> two) {
   __shared__ __align__(16) float sw[kWaves][Batch<NR, NARROW>::kFloats];
   __shared__ __align__(16) uint32_t sx[kWaves][kWave];
-  const Slot sl = slot_of(a.S, a.blocks);
+  const int which = blockIdx.x >= two.split ? 1 : 0;
+  const SumArgs &a = two.a[which];
+  const TX *__restrict__ X = two.X[which];
+  TO *__restrict__ out = two.out[which];
+  const Slot sl = slot_of(a.S, a.blocks, blockIdx.x - (which ? two.split : 0));
   const int slice = sl.slice, rb = sl.block;
   const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x >> 6);
   const int unit = a.unit0 + rb * kWaves + wave;
@@ -1270,6 +1284,8 @@ SumPlan sum_plan(int n_rows, int n_x, int E, int nv, int bytes) {
 // Parts of a row's edges in the dot products with v: in eights, so that an
 // XCD's part of v fits its L2; one where that leaves too few edges a part to
 // pay for reading the row of grad_out again (8), or where rows are short.
+// (Rows of 6.4 KB, 181 edges a row, 19 MB of v: 1, 8, 16, 24 parts 374, 153,
+// 166, 180 us; 138 edges a row, 52 MB: 879, 532, 477, 529.)
 int dot_parts(const Shape &s, int bytes) {
   const int64_t deg = s.E / (s.n_dst > 0 ? s.n_dst : 1);
   const int64_t v = static_cast<int64_t>(s.n_src) * s.K * s.C * bytes;
@@ -1329,32 +1345,38 @@ size_t ws_fwd_of(const Shape &s, bool train) {
 
 size_t ws_bwd_of(const Shape &s) {
   const size_t E = s.E, H = s.H, P = plane(s);
-  size_t part = sum_part_bytes(s.n_dst, s.n_src, s.E, 2 * s.H * s.D);
-  for (int width : {2 * s.H * s.D, s.K * s.C}) {
-    const size_t n = sum_part_bytes(s.n_src, s.n_dst, s.E, width);
-    if (n > part) part = n;
-  }
+  const size_t part = std::max(sum_part_bytes(s.n_dst, s.n_src, s.E, 2 * s.H * s.D) +
+                                   sum_part_bytes(s.n_src, s.n_dst, s.E, 2 * s.H * s.D),
+                               sum_part_bytes(s.n_src, s.n_dst, s.E, s.K * s.C));
   return align256(E * 2 * H * 4) + 2 * align256(E * H * 4) + 2 * align256(P * 2 * H * 4) + align256(P * H * 4) +
          align256(E * 4) + align256(static_cast<size_t>(s.n_dst) * H * 4) +
          align256(static_cast<size_t>(s.pieces) * H * 8) + part;
 }
 
 template <typename TX, typename TO, int VW, int NR, bool NARROW, bool MIX>
-void launch_sum(unsigned grid, int mode, hipStream_t st, const SumArgs &a, const TX *X, TO *out) {
-  if (mode == kScalar) gather_sum_kernel<TX, TO, VW, kScalar, NR, NARROW, MIX><<<grid, kThreads, 0, st>>>(a, X, out);
-  else if (mode == kOffset)
-    gather_sum_kernel<TX, TO, VW, kOffset, NR, NARROW, MIX><<<grid, kThreads, 0, st>>>(a, X, out);
-  else gather_sum_kernel<TX, TO, VW, kLong, NR, NARROW, MIX><<<grid, kThreads, 0, st>>>(a, X, out);
+void launch_sum(unsigned grid, int mode, hipStream_t st, const SumPair<TX, TO> &two) {
+  if (mode == kScalar) gather_sum_kernel<TX, TO, VW, kScalar, NR, NARROW, MIX><<<grid, kThreads, 0, st>>>(two);
+  else if (mode == kOffset) gather_sum_kernel<TX, TO, VW, kOffset, NR, NARROW, MIX><<<grid, kThreads, 0, st>>>(two);
+  else gather_sum_kernel<TX, TO, VW, kLong, NR, NARROW, MIX><<<grid, kThreads, 0, st>>>(two);
 }
 
-template <typename TX, typename TO>
-egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream_t st) {
-  if (a.n_rows == 0) return EGNN_OK;
+// What picks the kernel of a sum.
+struct SumKind {
+  int vw, mode;
+  bool mix, narrow, few;  // few: at most 8 planes
+  int64_t pieces;
+  bool operator==(const SumKind &o) const {
+    return vw == o.vw && mode == o.mode && mix == o.mix && narrow == o.narrow && few == o.few;
+  }
+};
+
+// Completes the arguments of a sum (slices, staging, pieces).
+template <typename TX, typename TO> SumKind plan_sum(SumArgs &a, const TX *X, const TO *out) {
+  SumKind k;
   // 16-byte vectors of a row; one may hold elements of several heads (mix)
   constexpr int V = 16 / sizeof(TX);
-  const int vw = a.width % V == 0 && a.ldx % V == 0 && aligned16(X) && aligned16(out) ? V : 1;
-  const bool mix = vw > 1 && a.Ch % V != 0;
-  const SumPlan p = sum_plan(a.n_rows, a.n_x, a.E, a.width / vw, vw * static_cast<int>(sizeof(TX)));
+  k.vw = a.width % V == 0 && a.ldx % V == 0 && aligned16(X) && aligned16(out) ? V : 1;
+  const SumPlan p = sum_plan(a.n_rows, a.n_x, a.E, a.width / k.vw, k.vw * static_cast<int>(sizeof(TX)));
   a.S = p.S;
   a.SV = p.SV;
   a.EPW = p.EPW;
@@ -1363,7 +1385,7 @@ egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream
   if (a.width == a.C && a.S > 1) {
     a.planes = 1;
     for (int i = 0; i < a.S; ++i) {
-      const int c0 = i * a.SV * vw, c1 = (i + 1) * a.SV * vw < a.width ? (i + 1) * a.SV * vw : a.width;
+      const int c0 = i * a.SV * k.vw, c1 = std::min((i + 1) * a.SV * k.vw, a.width);
       if (c0 < c1) a.planes = std::max(a.planes, (c1 - 1) / a.Ch - c0 / a.Ch + 1);
     }
   }
@@ -1371,37 +1393,91 @@ egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream
   const int round = p.EPW == 1 ? 8 : 4 * p.EPW, stage = a.planes <= 16 ? kWave : 16;
   if (round > stage) a.EPW = stage / 4;
   a.BE = stage / (a.EPW == 1 ? 8 : 4 * a.EPW) * (a.EPW == 1 ? 8 : 4 * a.EPW);
-  const int mode = a.EPW == 1                                                                       ? kScalar
-                   : static_cast<uint64_t>(a.n_x) * a.ldx * sizeof(TX) < (uint64_t(1) << 32) ? kOffset
-                                                                                                    : kLong;
+  k.mode = a.EPW == 1                                                                     ? kScalar
+           : static_cast<uint64_t>(a.n_x) * a.ldx * sizeof(TX) < (uint64_t(1) << 32) ? kOffset
+                                                                                     : kLong;
   a.units = static_cast<int>(a.n_rows + p.pieces);
-  const int most = kMaxBlocks / a.S;  // blocks a slice in one launch
-  for (a.unit0 = 0; a.unit0 < a.units; a.unit0 += most * kWaves) {
-    Timed t(st, name, a.unit0 ? 0.0 : 2.0 * a.E * a.width,
-            a.unit0 ? 0.0
-                    : static_cast<double>(a.E) * (4.0 * a.H + 4) + static_cast<double>(a.n_x) * a.width * sizeof(TX) +
-                          static_cast<double>(a.n_rows) * a.width * sizeof(TO));
-    const int left = (a.units - a.unit0 + kWaves - 1) / kWaves;
-    a.blocks = left < most ? left : most;
-    const unsigned grid = static_cast<unsigned>(a.blocks) * a.S;
-    // registers for the next edges' weights: as few as the heads allow
-    const bool narrow = a.planes > 16;
-    if (mix && !narrow) launch_sum<TX, TO, V, 16, false, true>(grid, mode, st, a, X, out);
-    else if (mix) launch_sum<TX, TO, V, 16, true, true>(grid, mode, st, a, X, out);
-    else if (vw > 1 && a.planes <= 8) launch_sum<TX, TO, V, 8, false, false>(grid, mode, st, a, X, out);
-    else if (vw > 1 && !narrow) launch_sum<TX, TO, V, 16, false, false>(grid, mode, st, a, X, out);
-    else if (vw > 1) launch_sum<TX, TO, V, 16, true, false>(grid, mode, st, a, X, out);
-    else if (!narrow) launch_sum<TX, TO, 1, 16, false, false>(grid, mode, st, a, X, out);
-    else launch_sum<TX, TO, 1, 16, true, false>(grid, mode, st, a, X, out);
-    EGNN_CHECK_LAUNCH();
-  }
-  if (p.pieces) {
-    Timed t(st, "attn_long_sum", 0.0, 0.0);
-    long_sum_kernel<TO><<<dim3(static_cast<unsigned>(p.pieces / 2), ceil_div(a.width, kThreads)), kThreads, 0,
-                                st>>>(a, out);
-    EGNN_CHECK_LAUNCH();
-  }
+  a.unit0 = 0;
+  a.blocks = (a.units + kWaves - 1) / kWaves;
+  k.mix = k.vw > 1 && a.Ch % V != 0;
+  k.narrow = a.planes > 16;
+  k.few = a.planes <= 8;  // registers for the next edges' weights: as few as the heads allow
+  k.pieces = p.pieces;
+  return k;
+}
+
+template <typename TX, typename TO>
+egnn_status launch_kind(const SumKind &k, unsigned grid, const SumPair<TX, TO> &two, hipStream_t st) {
+  constexpr int V = 16 / sizeof(TX);
+  if (k.mix && !k.narrow) launch_sum<TX, TO, V, 16, false, true>(grid, k.mode, st, two);
+  else if (k.mix) launch_sum<TX, TO, V, 16, true, true>(grid, k.mode, st, two);
+  else if (k.vw > 1 && k.few) launch_sum<TX, TO, V, 8, false, false>(grid, k.mode, st, two);
+  else if (k.vw > 1 && !k.narrow) launch_sum<TX, TO, V, 16, false, false>(grid, k.mode, st, two);
+  else if (k.vw > 1) launch_sum<TX, TO, V, 16, true, false>(grid, k.mode, st, two);
+  else if (!k.narrow) launch_sum<TX, TO, 1, 16, false, false>(grid, k.mode, st, two);
+  else launch_sum<TX, TO, 1, 16, true, false>(grid, k.mode, st, two);
+  EGNN_CHECK_LAUNCH();
   return EGNN_OK;
+}
+
+template <typename TX, typename TO> double sum_bytes(const SumArgs &a) {
+  return static_cast<double>(a.E) * (4.0 * a.H + 4) + static_cast<double>(a.n_x) * a.width * sizeof(TX) +
+         static_cast<double>(a.n_rows) * a.width * sizeof(TO);
+}
+
+template <typename TX, typename TO>
+egnn_status join_pieces(const SumKind &k, const SumArgs &a, TO *out, hipStream_t st) {
+  if (!k.pieces) return EGNN_OK;
+  Timed t(st, "attn_long_sum", 0.0, 0.0);
+  long_sum_kernel<TO><<<dim3(static_cast<unsigned>(k.pieces / 2), ceil_div(a.width, kThreads)), kThreads, 0, st>>>(
+      a, out);
+  EGNN_CHECK_LAUNCH();
+  return EGNN_OK;
+}
+
+template <typename TX, typename TO>
+egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream_t st) {
+  if (a.n_rows == 0) return EGNN_OK;
+  const SumKind k = plan_sum(a, X, out);
+  const int most = kMaxBlocks / a.S;  // blocks a slice in one launch
+  for (; a.unit0 < a.units; a.unit0 += most * kWaves) {
+    Timed t(st, name, a.unit0 ? 0.0 : 2.0 * a.E * a.width, a.unit0 ? 0.0 : sum_bytes<TX, TO>(a));
+    a.blocks = std::min((a.units - a.unit0 + kWaves - 1) / kWaves, most);
+    const unsigned grid = static_cast<unsigned>(a.blocks) * a.S;
+    const egnn_status r = launch_kind<TX, TO>(k, grid, SumPair<TX, TO>{{a, a}, {X, X}, {out, out}, grid}, st);
+    if (r != EGNN_OK) return r;
+  }
+  return join_pieces<TX, TO>(k, a, out, st);
+}
+
+// Two sums that need one kind of kernel share a launch; their pieces are
+// joined apart (each has its own part of the workspace).
+template <typename TX, typename TO>
+egnn_status run_two_sums(SumArgs a, const TX *Xa, TO *outa, const char *na, SumArgs b, const TX *Xb, TO *outb,
+                         const char *nb, const char *both, hipStream_t st) {
+  SumArgs a2 = a, b2 = b;
+  if (a.n_rows > 0 && b.n_rows > 0) {
+    const SumKind ka = plan_sum(a2, Xa, outa), kb = plan_sum(b2, Xb, outb);
+    const int64_t ga = (static_cast<int64_t>(a2.blocks) * a2.S + 7) & ~int64_t(7);
+    const int64_t gb = static_cast<int64_t>(b2.blocks) * b2.S;
+    // (rows of 1 KB: 3 MB of each, 0.54 M edges, 71 us apart and 61 together;
+    // 8 MB of each, 1.1 M edges, 171 and 191: their L2 lines displace each other)
+    const int64_t bytes = (static_cast<int64_t>(a.n_x) * a.width + static_cast<int64_t>(b.n_x) * b.width) *
+                          static_cast<int64_t>(sizeof(TX));
+    if (ka == kb && ga + gb <= kMaxBlocks && bytes <= kPairBytes) {
+      {
+        Timed t(st, both, 2.0 * a.E * (a.width + b.width), sum_bytes<TX, TO>(a2) + sum_bytes<TX, TO>(b2));
+        const egnn_status r =
+            launch_kind<TX, TO>(ka, static_cast<unsigned>(ga + gb),
+                                SumPair<TX, TO>{{a2, b2}, {Xa, Xb}, {outa, outb}, static_cast<unsigned>(ga)}, st);
+        if (r != EGNN_OK) return r;
+      }
+      const egnn_status r = join_pieces<TX, TO>(ka, a2, outa, st);
+      return r != EGNN_OK ? r : join_pieces<TX, TO>(kb, b2, outb, st);
+    }
+  }
+  const egnn_status r = run_sum<TX, TO>(a, Xa, outa, na, st);
+  return r != EGNN_OK ? r : run_sum<TX, TO>(b, Xb, outb, nb, st);
 }
 
 template <typename T, int VW, bool ONE, int NIT = kMaxNit>
@@ -1613,8 +1689,7 @@ egnn_status backward(const Shape &s, const egnn_graph *g, const T *q, const T *k
   m.width = 2 * s.H * s.D;
   m.scale = s.scale;
   m.part = part;
-  egnn_status r = run_sum<T, float>(m, k, gq, "attn_grad_q", st);
-  if (r != EGNN_OK) return r;
+  const SumArgs to_q = m;
   m.ptr = g->src_ptr;
   m.col = dst_src;
   m.row_of = g->src;
@@ -1623,8 +1698,11 @@ egnn_status backward(const Shape &s, const egnn_graph *g, const T *q, const T *k
   m.n_x = s.n_dst;
   m.ldx = s.ldq;
   m.w = dlp_src;
-  r = run_sum<T, float>(m, q, gk, "attn_grad_k", st);
+  m.part = part + sum_part_bytes(s.n_dst, s.n_src, s.E, m.width) / 4;  // both run at once
+  const egnn_status r =
+      run_two_sums<T, float>(to_q, k, gq, "attn_grad_q", m, q, gk, "attn_grad_k", "attn_grad_qk", st);
   if (r != EGNN_OK) return r;
+  m.part = part;
   m.ldx = static_cast<int64_t>(s.K) * s.C;
   m.w = w_src;
   m.H = s.H;

@@ -7,19 +7,30 @@
 //   out[d,k,c] = sum_e w[e,h(c)] v[src,k,c]
 //
 // Two shapes of work carry both directions:
-//   products   per edge and head, a dot of a destination's row with a source's row
-//              (the logits, and <grad_out, v> in the backward), with the row's softmax
-//              (or its backward) in the same block;
-//   sums       per row and column, a weighted sum of gathered rows (out, and the
-//              gradients of q, k and v; the latter two over edges grouped by source).
+//   products   per edge and head, a dot of a destination's row with a source's
+//              row: the logits, with the row's softmax in the same block, and
+//              <grad_out, v>, whose softmax backward is a launch of its own;
+//   sums       per row and column, a weighted sum of gathered rows: out, and the
+//              gradients of q, k and v (of k and v over edges grouped by source).
 //
-// Rows are handled by one block (products) or one wave per column slice
-// (sums).  A row longer than the kernel's limit T is cut at the multiples of T
-// of the edge array, so pieces need no list and no host knowledge of the row
-// lengths: window x = [xT, (x+1)T) holds at most the end of one long row
-// (piece 2x: the row that owns edge xT) and the start of another (piece 2x+1:
-// the row that owns the window's last edge, if it starts inside the window).
-// Pieces are joined by a later launch, in edge order.
+// What bounds them: not HBM (the operands are some tens of MB) but the gathered
+// rows, edges x row bytes, through the L2s and the vector caches.  So a sum is
+// sliced by columns and a product's rows are cut by source, one slice or part
+// an XCD, so that each 4 MB L2 holds its own share of the gathered array: the
+// rows then come from L2 rather than over the fabric (HfO2-like cell, 544,000
+// edges of 6.4 KB: out 340 us unsliced loads with vector addressing, 165 us
+// now, 21 TB/s, about 70% of the L2s' line rate; dots 374 us in one part, 153
+// in eight).  In bf16 the conversion to fp32 (two instructions a pair) beside
+// the multiply-adds is the limit: vector units busy 93% in out of the
+// GeSbTe-like cell (1.11 M edges, 471 us).
+//
+// Rows are handled by one block (logits, softmax) or one wave per slice or
+// part (sums, dots).  A row longer than the launch's limit T is cut at the
+// multiples of T of the edge array, so pieces need no list and no host
+// knowledge of the row lengths: window x = [xT, (x+1)T) holds at most the end
+// of one long row (piece 2x: the row that owns edge xT) and the start of
+// another (piece 2x+1: the row that owns the window's last edge, if it starts
+// inside the window).  Pieces are joined by a later launch, in edge order.
 #include <algorithm>
 #include <cmath>
 
@@ -330,7 +341,7 @@ template <int CTRL> __device__ inline float dpp_move(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
 }
 
-// v + v of the lane that differs in bit `bit` only
+// v plus the value in the lane that differs in bit `bit` only
 __device__ inline float add_across(float v, int bit) {
   if (bit == 5) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -368,9 +379,9 @@ __device__ inline void team_sum(float (&dot)[U], const Team &tm) {
     for (int u = 0; u < U; ++u) dot[u] = add_across(dot[u], bit);
 }
 
-// put(i, h, dot, first) for edges i = i_first + es + EPW-wide steps of
-// `stride` below cnt, dot = sum over the head's vectors of A . B[scol[i]] (row
-// 0 for a source of -1).  A stays in registers, NIT vectors a lane; what does
+// put(i, h, dot, first) for the edges i < cnt of i_first, i_first + stride, ...
+// (and, where a wave takes several at once, those that follow each), dot = sum
+// over the head's vectors of A . B[scol[i]] (row 0 for a source of -1).  A stays in registers, NIT vectors a lane; what does
 // not fit is added by further rounds (first = false).  ONE: a wave takes one
 // edge at a time, so the row's address is scalar work.
 template <typename TA, typename TB, int VW, int NIT, bool ONE, typename Put>
@@ -768,7 +779,6 @@ __global__ void __launch_bounds__(kThreads) logit_grad_kernel(GradArgs a) {
   __shared__ float red[kWaves][kWave];
   __shared__ float2 tt[kMaxHeads];
   __shared__ float slam[kMaxHeads];
-  if (threadIdx.x < static_cast<unsigned>(a.H)) slam[threadIdx.x] = a.lam[threadIdx.x];
   int d, b, e;
   const int p = static_cast<int>(blockIdx.x) - a.n_dst;
   if (p < 0) {
@@ -787,6 +797,7 @@ __global__ void __launch_bounds__(kThreads) logit_grad_kernel(GradArgs a) {
     e = pc.end;
   }
   const int H = a.H, Hp = 1 << a.Hpl, pitch = 2 * H + 1;
+  if (threadIdx.x < static_cast<unsigned>(H)) slam[threadIdx.x] = a.lam[threadIdx.x];  // null only without edges
   const int h = threadIdx.x & (Hp - 1), r0 = threadIdx.x >> a.Hpl, R = kThreads >> a.Hpl;
   const bool again = p >= 0 || e - b > a.T;  // u does not stay in LDS until the row's sums are known
   float t0 = 0.0f, t1 = 0.0f;
@@ -995,8 +1006,9 @@ enum { kScalar, kOffset, kLong };
 // cost as much as others).  SAFE skips weights of 0, so that what such a row
 // of X holds stays out.
 template <typename TX, int VW, int MODE, int NR, bool NARROW, bool MIX, bool SAFE>
-__device__ inline void gather_rows(const SumArgs &a, const TX *X, const float *planes, int n_planes, int b, int e, int c,
-                                   const int (&head)[VW], int grp, bool on, int lane, float *sw, uint32_t *sx, float (&acc)[VW]) {
+__device__ inline void gather_rows(const SumArgs &a, const TX *X, const float *planes, int n_planes, int b, int e,
+                                   int c, const int (&head)[VW], int grp, bool on, int lane, float *sw, uint32_t *sx,
+                                   float (&acc)[VW]) {
   constexpr int U = MODE == kScalar ? 8 : 4;  // edges a group has in flight
   const int step = MODE == kScalar ? U : a.EPW * U;
   const uint32_t pitch = static_cast<uint32_t>(a.ldx * sizeof(TX));
@@ -1122,7 +1134,8 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(const SumPair<TX, 
   float acc[VW];
 #pragma unroll
   for (int k = 0; k < VW; ++k) acc[k] = 0.0f;
-  gather_rows<TX, VW, MODE, NR, NARROW, MIX, false>(a, X, planes, n_planes, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
+  gather_rows<TX, VW, MODE, NR, NARROW, MIX, false>(a, X, planes, n_planes, b, e, c, head, grp, on, lane, sw[wave],
+                                                    sx[wave], acc);
   // A sum that is finite had no infinity or NaN in it, so its weights of 0
   // added 0.  One that is not is taken again with those edges left out.
   bool odd = false;
@@ -1131,7 +1144,8 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(const SumPair<TX, 
   if (__any(odd)) {
 #pragma unroll
     for (int k = 0; k < VW; ++k) acc[k] = 0.0f;
-    gather_rows<TX, VW, MODE, NR, NARROW, MIX, true>(a, X, planes, n_planes, b, e, c, head, grp, on, lane, sw[wave], sx[wave], acc);
+    gather_rows<TX, VW, MODE, NR, NARROW, MIX, true>(a, X, planes, n_planes, b, e, c, head, grp, on, lane, sw[wave],
+                                                     sx[wave], acc);
   }
   if constexpr (MODE != kScalar) {
     float sum[VW];
@@ -1196,7 +1210,7 @@ struct Shape {
 // n_rows rows.  Enough units fill the chip by themselves, and a piece costs one
 // that mostly finds nothing to do; few are cut at `few`.  A small graph of
 // ordinary rows is not cut at all: that saves the launches that join pieces
-// (64 atoms, 2,900 edges, forward: four launches 29 us, two @@ us).
+// (64 atoms, 2,900 edges, forward: 26 us in four launches, 18 in two).
 int piece_edges(int64_t units, int n_rows, int E, int few) {
   if (E <= 4096 && E <= static_cast<int64_t>(128) * n_rows) return E > 0 ? E : 1;
   return units >= 4096 ? 4096 : few;
@@ -1227,7 +1241,8 @@ egnn_status make_shape_of(const egnn_attn_desc *d, const egnn_graph *g, Shape *s
   s->ldv = d->v_stride ? d->v_stride : vals;
   EGNN_REQUIRE(s->ldq >= qk && s->ldk >= qk, "q and k row strides must be 0 or at least 2 n_heads head_dim");
   EGNN_REQUIRE(s->ldv >= vals, "v row stride must be 0 or at least (lmax+1)^2 C");
-  EGNN_REQUIRE(s->ldq <= kMaxStride && s->ldk <= kMaxStride && s->ldv <= kMaxStride, "row strides are at most 2^29 elements");
+  EGNN_REQUIRE(s->ldq <= kMaxStride && s->ldk <= kMaxStride && s->ldv <= kMaxStride,
+               "row strides are at most 2^29 elements");
   EGNN_REQUIRE(g, "graph is null");
   EGNN_REQUIRE(g->n_dst >= 0 && g->n_src >= 0, "negative row counts");
   EGNN_REQUIRE(g->n_edges >= 0, "negative edge count");

@@ -299,7 +299,8 @@ egnn_status egnn_edge_update_bwd(const egnn_layer_desc *d, const egnn_graph *g, 
  * statistics are fp32; out is rounded once.  Results are bit-identical
  * between runs.  out must not alias an input.
  * Limits: H 1..32, D 1..256, C 1..1024 a multiple of H, lmax 0..8; 2^28
- * edges, 2^21 rows and sources (EGNN_E_UNSUPPORTED beyond).
+ * edges, 2^21 rows and sources (EGNN_E_UNSUPPORTED beyond), row strides up
+ * to 2^29 elements.
  *
  * saved (NULL for inference) receives what the backward reads; the workspace
  * is ws_infer bytes without it, ws_train with it (which also serves the

@@ -82,6 +82,20 @@ CASES = {
     "long_rows": Case((5, 512, 1024, 3, 700, 0, 256, 1), 90, 1, 16, 8, 8, mask=True, p=0.1),
     "long_rows_many_heads": Case((64, 65, 130, 2, 300), 40, 0, 64, 32, 4, p=0.1),
     "long_rows_two_maps": Case((513, 1, 1100), 50, 2, 6, 1, 3),
+    # a small graph is not cut: one block walks its long row in steps
+    "steps_in_a_row": Case((700, 3, 0, 300) + (20,) * 36, 60, 1, 16, 8, 8, p=0.2),
+    "steps_in_a_row_bf16": Case((900,) + (15,) * 40, 60, 2, 32, 4, 8, "bf16", mask=True),
+    # many rows: cut at 4,096 edges only, so blocks take steps and pieces are joined
+    "many_rows_and_a_long_one": Case((3,) * 500 + (9000,) + (2, 0, 5) * 200, 300, 0, 8, 2, 4, p=0.1),
+    # long component-free rows: slices that meet a few heads each
+    "wide_invariants": Case(varied(12, 9, 20), 15, 0, 1024, 16, 128, p=0.1),
+    "wide_invariants_bf16": Case(varied(13, 9, 20), 15, 0, 1024, 32, 64, "bf16"),
+    # vectors that hold several heads, more than 16 of them
+    "mixed_heads": Case(varied(14, 8, 30), 20, 1, 64, 32, 2, p=0.1),
+    "mixed_heads_bf16": Case(varied(15, 8, 30), 20, 3, 48, 16, 4, "bf16", mask=True),
+    # half vectors
+    "pairs": Case(varied(16, 8, 30), 20, 2, 36, 6, 6),
+    "quads_bf16": Case(varied(17, 8, 30), 20, 2, 32, 8, 4, "bf16"),
     # one source in every edge: the backward's long rows
     "one_source": Case(varied(11, 40, 60), 1, 1, 16, 2, 8, p=0.1),
 }
@@ -265,6 +279,62 @@ def test_strided_and_unaligned_rows(dev, dtype):
         within(host(out2), res["out"], bnd["out"], d["dt"], "out")
         for m in NAMES:
             within(host(got2[m]), res[m], bnd[m], None, m)
+
+
+def test_offsets_beyond_32_bits(dev):
+    """Rows 2^27 elements apart (an array of more than 4 GB): bit-identical to packed rows."""
+    case = dataclasses.replace(CASES["cell"], degrees=varied(1, 12, 12), n_src=12, lmax=0, C=16)
+    d = make(case, dev)
+    buf = eg.AttnBuffers(d["desc"], d["graph"])
+    out, _ = forward(d, buffers=buf)
+    got = backward(d, buf)
+    far = {}
+    for n in ("q", "k", "v"):
+        rows, width = d[n].shape[0], d[n][0].numel()
+        a = torch.empty((rows - 1) * 2**27 + width, device=dev).as_strided((rows, width), (2**27, 1))
+        a.copy_(d[n].view(rows, width))
+        far[n] = a.as_strided(d[n].shape, (2**27, *d[n].stride()[1:]))
+    e = dict(d, **far)
+    out2, _ = forward(e, buffers=buf)
+    got2 = backward(e, buf)
+    assert torch.equal(out, out2) and all(torch.equal(got[m], got2[m]) for m in NAMES)
+
+
+def test_unsorted_sources_and_doubled_edges(dev):
+    """Sources in any order and the same edge twice: the graph need only be grouped by destination."""
+    case = dataclasses.replace(CASES["hfo2_shape"], degrees=(90, 150, 200, 40) * 8, n_src=300)
+    d = make(case, dev)
+    d["src"][5:9] = d["src"][4]
+    d["graph"] = eg.Graph.from_csr(d["row_ptr"], d["src"], n_src=case.n_src, group=True)
+    buf = eg.AttnBuffers(d["desc"], d["graph"])
+    out, _ = forward(d, buffers=buf)
+    got = backward(d, buf)
+    res, bnd = oracle_of(case, d)
+    within(host(out), res["out"], bnd["out"], d["dt"], "out")
+    for n in NAMES:
+        within(host(got[n]), res[n], bnd[n], None, n)
+
+
+def test_no_edges_without_operands(dev):
+    """A graph without edges through the C ABI with every operand NULL that the header lets be: gradients of zero."""
+    g = _lib.EgnnGraph()
+    ptr = torch.zeros(4, dtype=torch.int32, device=dev)
+    g.n_dst, g.n_src, g.n_edges = 3, 3, 0
+    g.row_ptr = g.src_ptr = ptr.data_ptr()
+    d = eg.attn_desc(1, 8, 2, 4)
+    s, i, t = (ct.c_size_t() for _ in range(3))
+    lib = _lib.load()
+    assert lib.egnn_diff_attention_sizes(ct.byref(d), ct.byref(g), ct.byref(s), ct.byref(i), ct.byref(t)) == 0
+    ws = torch.empty(max(i.value, t.value, 1), dtype=torch.uint8, device=dev)
+    outs = [torch.full(sh, 9.0, device=dev) for sh in ((3, 4, 8), (3, 2, 2, 4), (3, 2, 2, 4), (3, 4, 8), (2,))]
+    st = ct.c_void_p(torch.cuda.current_stream().cuda_stream)
+    p = lambda x: ct.c_void_p(x.data_ptr())  # noqa: E731
+    assert lib.egnn_diff_attention_fwd(ct.byref(d), ct.byref(g), None, None, None, None, None, None, None, p(outs[0]),
+                                       None, p(ws), ws.numel(), st) == 0
+    assert lib.egnn_diff_attention_bwd(ct.byref(d), ct.byref(g), None, None, None, None, None, None, None,
+                                       *map(p, outs[1:]), None, p(ws), ws.numel(), st) == 0
+    torch.cuda.synchronize()
+    assert all(bool((o == 0).all()) for o in outs)
 
 
 def test_rows_of_a_longer_array(dev):

@@ -122,8 +122,11 @@ __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v);
 
 // A byte offset the wave shares, kept on the scalar unit (the compiler
 // otherwise folds the row's product into a 64-bit multiply-add per lane).
+// Unoptimised code keeps no value there.
 __device__ inline uint64_t scalar(uint64_t v) {
+#ifdef __OPTIMIZE__
   asm("" : "+s"(v));
+#endif
   return v;
 }
 

@@ -627,18 +627,23 @@ __global__ void __launch_bounds__(kThreads) long_weights_kernel(LogitArgs a) {
   const int H2 = 2 * a.H, Hp = 1 << a.Hpl;
   const int col = threadIdx.x & (Hp - 1), r0 = threadIdx.x >> a.Hpl, R = kThreads >> a.Hpl;
   const int n = piece_count(b, e, a.TP);
-  float M = -INFINITY;
+  float own = -INFINITY, S = 0.0f;  // of this thread's pieces
   if (col < H2)
-    for (int i = r0; i < n; i += R)
-      M = fmaxf(M, a.piece_stats[static_cast<int64_t>(piece_id(b, a.TP, i)) * H2 + col].x);
-  M = column_reduce(M, Hp, red, MaxOp());
-  float S = 0.0f;
-  if (col < H2 && M != -INFINITY)
-    for (int i = r0; i < n; i += R) {
-      const float2 st = a.piece_stats[static_cast<int64_t>(piece_id(b, a.TP, i)) * H2 + col];
-      if (st.x != -INFINITY) S += st.y * __expf(st.x - M);
+    for (int i0 = r0; i0 < n; i0 += 8 * R) {
+      float2 st[8];  // loaded together
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        st[u] = a.piece_stats[static_cast<int64_t>(piece_id(b, a.TP, min(i0 + u * R, n - 1))) * H2 + col];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (i0 + u * R >= n || st[u].x == -INFINITY) continue;
+        const float top = fmaxf(own, st[u].x);
+        S = (own == -INFINITY ? 0.0f : S * __expf(own - top)) + st[u].y * __expf(st[u].x - top);
+        own = top;
+      }
     }
-  S = column_reduce(S, Hp, red, SumOp());
+  const float M = column_reduce(own, Hp, red, MaxOp());
+  S = column_reduce(own == -INFINITY ? 0.0f : S * __expf(own - M), Hp, red, SumOp());
   if (r0 == 0 && col < H2) fin[col] = finish_stats(M, S);
   __syncthreads();
   edge_weights(a, fin, pc.begin, pc.end - pc.begin);
@@ -863,10 +868,16 @@ __global__ void __launch_bounds__(kThreads) long_grad_kernel(GradArgs a) {
   const int n = piece_count(b, e, a.TP);
   float t0 = 0.0f, t1 = 0.0f;
   if (h < H)
-    for (int i = r0; i < n; i += R) {
-      const float2 t = a.piece_t[static_cast<int64_t>(piece_id(b, a.TP, i)) * H + h];
-      t0 += t.x;
-      t1 += t.y;
+    for (int i0 = r0; i0 < n; i0 += 8 * R) {
+      float2 t[8];  // loaded together
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        t[u] = a.piece_t[static_cast<int64_t>(piece_id(b, a.TP, min(i0 + u * R, n - 1))) * H + h];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        t0 += i0 + u * R < n ? t[u].x : 0.0f;
+        t1 += i0 + u * R < n ? t[u].y : 0.0f;
+      }
     }
   t0 = column_reduce(t0, Hp, red, SumOp());
   t1 = column_reduce(t1, Hp, red, SumOp());
@@ -1170,10 +1181,12 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(const SumPair<TX, 
   Vec<TO, VW>::st(out + static_cast<int64_t>(row) * a.width + c, acc);
 }
 
-// Long rows: the pieces' sums, added in edge order.  One block per window and
-// 256 columns; it acts for the long row that starts in its window, if any.
+// Long rows: the pieces' sums added in a fixed order.  One block per window and
+// 64 columns, a wave a quarter of the pieces; it acts for the long row that
+// starts in its window, if any.
 template <typename TO>
 __global__ void __launch_bounds__(kThreads) long_sum_kernel(SumArgs a, TO *__restrict__ out) {
+  __shared__ float red[kWaves][kWave];
   const int total = min(max(a.ptr[a.n_rows], 0), a.E);
   const int64_t w0 = static_cast<int64_t>(blockIdx.x) * a.T;
   if (w0 >= total) return;
@@ -1182,18 +1195,24 @@ __global__ void __launch_bounds__(kThreads) long_sum_kernel(SumArgs a, TO *__res
   int b, e;
   row_bounds(a.ptr, row, a.E, &b, &e);
   if (e - b <= a.T || b < w0) return;
-  const int c = blockIdx.y * kThreads + threadIdx.x;
-  if (c >= a.width) return;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+  const int c = blockIdx.y * kWave + lane, cc = min(c, a.width - 1);
   const int n = piece_count(b, e, a.T);
+  const int upto = static_cast<int>(static_cast<int64_t>(n) * (wave + 1) / kWaves);
   float s = 0.0f;
-  for (int i0 = 0; i0 < n; i0 += 8) {
+  for (int i0 = static_cast<int>(static_cast<int64_t>(n) * wave / kWaves); i0 < upto; i0 += 8) {
     float v[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      v[u] = a.part[static_cast<int64_t>(piece_id(b, a.T, min(i0 + u, n - 1))) * a.width + c];
+      v[u] = a.part[static_cast<int64_t>(piece_id(b, a.T, min(i0 + u, n - 1))) * a.width + cc];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) s += i0 + u < n ? v[u] : 0.0f;
+    for (int u = 0; u < 8; ++u) s += i0 + u < upto ? v[u] : 0.0f;
   }
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave != 0 || c >= a.width) return;
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i) s += red[i][lane];
   Store<TO>::st(out + static_cast<int64_t>(row) * a.width + c, s * a.scale);
 }
 
@@ -1211,12 +1230,15 @@ struct Shape {
 
 // Edges beyond which a row is cut into pieces, for `units` waves over
 // n_rows rows.  Enough units fill the chip by themselves, and a piece costs one
-// that mostly finds nothing to do; few are cut at `few`.  A small graph of
+// that mostly finds nothing to do; few rows are cut at 64 edges (one row over
+// 8,064 atoms: logits 20 us at 256, 9 at 64).  A small graph of
 // ordinary rows is not cut at all: that saves the launches that join pieces
 // (64 atoms, 2,900 edges, forward: 26 us in four launches, 18 in two).
-int piece_edges(int64_t units, int n_rows, int E, int few) {
+int piece_edges(int64_t units, int n_rows, int E) {
   if (E <= 4096 && E <= static_cast<int64_t>(128) * n_rows) return E > 0 ? E : 1;
-  return units >= 4096 ? 4096 : few;
+  if (units >= 4096) return 4096;
+  const int even = static_cast<int>((E / 2048 + 63) & ~int64_t(63));  // at most about 2,048 windows
+  return even < 64 ? 64 : even < 4096 ? even : 4096;
 }
 
 egnn_status make_shape_of(const egnn_attn_desc *d, const egnn_graph *g, Shape *s) {
@@ -1259,7 +1281,7 @@ egnn_status make_shape_of(const egnn_attn_desc *d, const egnn_graph *g, Shape *s
   s->E = static_cast<int>(g->n_edges);
   const int fit = 4096 / (2 * s->H);  // 16 KB of logits
   s->T = fit < 64 ? 64 : fit > 512 ? 512 : fit;
-  s->TP = piece_edges(static_cast<int64_t>(s->n_dst) * kWaves, s->n_dst, s->E, 64);
+  s->TP = piece_edges(static_cast<int64_t>(s->n_dst) * kWaves, s->n_dst, s->E);
   s->pieces = s->E > s->TP ? 2 * ((static_cast<int64_t>(s->E) + s->TP - 1) / s->TP) : 0;
   return EGNN_OK;
 }
@@ -1294,7 +1316,7 @@ SumPlan sum_plan(int n_rows, int n_x, int E, int nv, int bytes) {
     }
   }
   p.EPW = kWave / p.SV < 16 ? kWave / p.SV : 16;
-  p.T = piece_edges(static_cast<int64_t>(n_rows) * p.S, n_rows, E, 128);
+  p.T = piece_edges(static_cast<int64_t>(n_rows) * p.S, n_rows, E);
   p.pieces = E > p.T ? 2 * ((static_cast<int64_t>(E) + p.T - 1) / p.T) : 0;
   return p;
 }
@@ -1447,7 +1469,7 @@ template <typename TX, typename TO>
 egnn_status join_pieces(const SumKind &k, const SumArgs &a, TO *out, hipStream_t st) {
   if (!k.pieces) return EGNN_OK;
   Timed t(st, "attn_long_sum", 0.0, 0.0);
-  long_sum_kernel<TO><<<dim3(static_cast<unsigned>(k.pieces / 2), ceil_div(a.width, kThreads)), kThreads, 0, st>>>(
+  long_sum_kernel<TO><<<dim3(static_cast<unsigned>(k.pieces / 2), ceil_div(a.width, kWave)), kThreads, 0, st>>>(
       a, out);
   EGNN_CHECK_LAUNCH();
   return EGNN_OK;
@@ -1630,7 +1652,7 @@ egnn_status backward(const Shape &s, const egnn_graph *g, const T *q, const T *k
     const int vw = std::min(vec_width<T>(Ch, s.ldv, v), aligned16(go) ? V : 1);
     a.team = make_team(s.K, s.H, Ch / vw);
     a.parts = dot_parts(s, sizeof(T));
-    a.T = piece_edges(static_cast<int64_t>(s.n_dst) * a.parts, s.n_dst, s.E, 128);
+    a.T = piece_edges(static_cast<int64_t>(s.n_dst) * a.parts, s.n_dst, s.E);
     const int64_t pieces = s.E > a.T ? 2 * ((static_cast<int64_t>(s.E) + a.T - 1) / a.T) : 0;
     a.units = static_cast<int>(s.n_dst + pieces);
     const int most = kMaxBlocks / a.parts;

@@ -53,7 +53,6 @@ constexpr int64_t kMaxStride = 1 << 29;    // a row's pitch in bytes is counted 
 constexpr int64_t kSliceBytes = 3200000;   // of X in one XCD's L2
 constexpr int64_t kPartBytes = 3600000;    // of v in one XCD's L2 (dot products)
 constexpr int64_t kPairBytes = 8000000;    // of both X of two sums that share a launch
-constexpr int kMinSlice = 16;              // vectors of the narrowest slice
 
 // ------------------------------------------------------------------ helpers
 
@@ -275,14 +274,17 @@ __device__ inline void for_decisions(int b, int cnt, int H, const Drop &dr, F f)
 }
 
 // Block b's slice (or part) of `slices`, and its number among the slice's
-// `blocks` blocks.  Consecutive blocks go to the eight XCDs in turn, so a slice
-// stays on one XCD (slices 1, 2, 4, 8 or a multiple of 8, eight at a time).
+// `blocks` blocks.  Consecutive blocks go to the eight XCDs in turn; eight
+// slices at a time keep one XCD each, and the last r = slices % 8 (1, 2 or 4)
+// are dealt over all XCDs, 8 / r to a slice, so that none idles.
 struct Slot {
   int slice, block;
 };
 __device__ inline Slot slot_of(int slices, int blocks, int b) {
-  if (slices <= 8) return Slot{b % slices, b / slices};
-  return Slot{((b >> 3) / blocks) * 8 + (b & 7), (b >> 3) % blocks};
+  const int full = slices >> 3, r = slices & 7, t = b - full * 8 * blocks;
+  if (t < 0) return Slot{((b >> 3) / blocks) * 8 + (b & 7), (b >> 3) % blocks};
+  if (r == 0) return Slot{slices, 0};  // padding behind the last slice
+  return Slot{full * 8 + t % r, t / r};
 }
 
 // ------------------------------------------------------------------ products
@@ -1305,13 +1307,16 @@ SumPlan sum_plan(int n_rows, int n_x, int E, int nv, int bytes) {
     p.S = 8 * ((nv + 8 * kWave - 1) / (8 * kWave));
     while ((p.SV = ((nv + p.S - 1) / p.S + 3) & ~3) > kWave) p.S += 8;
     // Where an XCD's L2 (4 MB) does not hold its slice of X, narrower ones in
-    // whole lines (eight vectors) that it does hold, if there are such.
+    // whole lines (eight vectors) that it does hold: of 48, 32, 24 and 16 the
+    // first that fills most lanes (64, 64, 48, 64 of 64) and whose number is
+    // one that slot_of spreads evenly.
     if (static_cast<int64_t>(n_x) * p.SV * bytes > kSliceBytes) {
-      int SV = (p.SV - 1) & ~7;
-      while (SV > kMinSlice && static_cast<int64_t>(n_x) * SV * bytes > kSliceBytes) SV -= 8;
-      if (SV >= kMinSlice && static_cast<int64_t>(n_x) * SV * bytes <= kSliceBytes) {
+      for (const int SV : {32, 16, 48, 24}) {
+        const int used = (nv + SV - 1) / SV, r = used & 7;
+        if (SV >= p.SV || static_cast<int64_t>(n_x) * SV * bytes > kSliceBytes || (r & (r - 1)) != 0) continue;
         p.SV = SV;
-        p.S = 8 * ((nv + 8 * SV - 1) / (8 * SV));
+        p.S = used;
+        break;
       }
     }
   }

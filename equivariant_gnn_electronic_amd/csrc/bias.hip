@@ -159,20 +159,20 @@ __global__ void __launch_bounds__(kThreads) bias_bwd_kernel(const float *__restr
   __syncthreads();
   for (int i = threadIdx.x; i < B * mt; i += blockDim.x) {
     const int b = i / mt, cc = i - b * mt;
-    float s = 0.0f;
+    double s = 0.0;  // thousands of short sums are joined: in 64 bits that adds no error to theirs
     for (int k = 0; k < copies; ++k) s += tab[(k * B + b) * Mt + cc];
-    part[(static_cast<int64_t>(blockIdx.x) * B + b) * M + c0 + cc] = s;
+    part[(static_cast<int64_t>(blockIdx.x) * B + b) * M + c0 + cc] = static_cast<float>(s);
   }
 }
 
 // grad_table[i] = sum over the partial tables: 32 threads an entry, in a fixed order
 __global__ void __launch_bounds__(kThreads) bias_sum_kernel(const float *__restrict__ part, int n_part, int n,
                                                             float *__restrict__ out) {
-  __shared__ float red[32][9];
+  __shared__ double red[32][9];
   const int col = threadIdx.x & 7, r = threadIdx.x >> 3;
   const int i = blockIdx.x * 8 + col;
   const float *p = part + (i < n ? i : n - 1);
-  float s = 0.0f;
+  double s = 0.0;
   for (int p0 = r; p0 < n_part; p0 += 32 * 8) {
     float v[8];
 #pragma unroll
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) bias_sum_kernel(const float *__restr
   if (r == 0 && i < n) {
 #pragma unroll
     for (int k = 1; k < 32; ++k) s += red[k][col];
-    out[i] = s;
+    out[i] = static_cast<float>(s);
   }
 }
 

@@ -231,12 +231,24 @@ __device__ inline float column_reduce(float v, int Hp, float (*red)[kWave], F f)
   for (int i = 1; i < kWaves; ++i) r = f(r, red[i][lane]);
   return r;
 }
+// exp(x), x <= 0 (or NaN): 2^t with t = x log2 e, whose rounding error r is
+// put back as a factor 1 + r ln 2.  Within 2 ulp for any x, where 2^t alone is
+// off by |x| / 2 ulp; infinity and what underflows give 0.
+__device__ inline float exp_of(float x) {
+  constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f, kLn2 = 0.693147181f;  // log2 e in two parts
+  x = x < -150.0f ? -150.0f : x;
+  const float t = x * kHi;
+  const float r = fmaf(x, kLo, fmaf(x, kHi, -t));
+  const float y = __builtin_amdgcn_exp2f(t);
+  return fmaf(y, r * kLn2, y);
+}
+
 struct MaxOp { __device__ float operator()(float a, float b) const { return fmaxf(a, b); } };
 struct SumOp { __device__ float operator()(float a, float b) const { return a + b; } };
 
 // softmax weight of a logit: (M, 1/S) of its row.  Rows with nothing left have
 // M = 0, 1/S = 0; a masked logit is -inf and gives 0.
-__device__ inline float weight_of(float l, float2 st) { return __expf(l - st.x) * st.y; }
+__device__ inline float weight_of(float l, float2 st) { return exp_of(l - st.x) * st.y; }
 
 __device__ inline float2 finish_stats(float M, float S) {
   if (M == -INFINITY) return make_float2(0.0f, 0.0f);
@@ -573,8 +585,8 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *
     const float Mn = fmaxf(M, column_reduce(Mc, Hp, red, MaxOp()));
     float Sc = 0.0f;
     if (col < H2 && Mn != -INFINITY)
-      for (int i = r0; i < cnt; i += R) Sc += __expf(lg[i * pitch + col] - Mn);
-    S = (M == -INFINITY ? 0.0f : S * __expf(M - Mn)) + column_reduce(Sc, Hp, red, SumOp());
+      for (int i = r0; i < cnt; i += R) Sc += exp_of(lg[i * pitch + col] - Mn);
+    S = (M == -INFINITY ? 0.0f : S * exp_of(M - Mn)) + column_reduce(Sc, Hp, red, SumOp());
     M = Mn;
   }
   if (p >= 0) {
@@ -640,12 +652,12 @@ __global__ void __launch_bounds__(kThreads) long_weights_kernel(LogitArgs a) {
       for (int u = 0; u < 8; ++u) {
         if (i0 + u * R >= n || st[u].x == -INFINITY) continue;
         const float top = fmaxf(own, st[u].x);
-        S = (own == -INFINITY ? 0.0f : S * __expf(own - top)) + st[u].y * __expf(st[u].x - top);
+        S = (own == -INFINITY ? 0.0f : S * exp_of(own - top)) + st[u].y * exp_of(st[u].x - top);
         own = top;
       }
     }
   const float M = column_reduce(own, Hp, red, MaxOp());
-  S = column_reduce(own == -INFINITY ? 0.0f : S * __expf(own - M), Hp, red, SumOp());
+  S = column_reduce(own == -INFINITY ? 0.0f : S * exp_of(own - M), Hp, red, SumOp());
   if (r0 == 0 && col < H2) fin[col] = finish_stats(M, S);
   __syncthreads();
   edge_weights(a, fin, pc.begin, pc.end - pc.begin);
@@ -688,7 +700,11 @@ __global__ void __launch_bounds__(kThreads) value_dots_kernel(DotArgs a, const f
   }
   b = uniform(b);
   e = uniform(e);
-  if (a.parts > 1) {
+  if (unit >= a.n_dst) {  // a piece's sources are near each other already
+    const int64_t len = e - b;
+    e = uniform(b + static_cast<int>(len * (sl.slice + 1) / a.parts));
+    b = uniform(b + static_cast<int>(len * sl.slice / a.parts));
+  } else if (a.parts > 1) {
     const int from = static_cast<int>(static_cast<int64_t>(a.n_src) * sl.slice / a.parts);
     const int to = static_cast<int>(static_cast<int64_t>(a.n_src) * (sl.slice + 1) / a.parts);
     int below = 0, upto = 0;
@@ -1230,17 +1246,19 @@ struct Shape {
   int64_t pieces;
 };
 
-// Edges beyond which a row is cut into pieces, for `units` waves over
-// n_rows rows.  Enough units fill the chip by themselves, and a piece costs one
-// that mostly finds nothing to do; few rows are cut at 64 edges (one row over
-// 8,064 atoms: logits 20 us at 256, 9 at 64).  A small graph of
+// Edges beyond which a row is cut into pieces, for `units` waves over n_rows
+// rows.  Enough units fill the chip by themselves, and a piece costs one that
+// mostly finds nothing to do; with fewer, rows of up to twice the mean stay
+// whole; with few, rows are cut into about 2,048 pieces of 64 edges or more
+// (one row over 8,064 atoms: logits 20 us at 256, 9 at 64).  A small graph of
 // ordinary rows is not cut at all: that saves the launches that join pieces
 // (64 atoms, 2,900 edges, forward: 26 us in four launches, 18 in two).
 int piece_edges(int64_t units, int n_rows, int E) {
   if (E <= 4096 && E <= static_cast<int64_t>(128) * n_rows) return E > 0 ? E : 1;
   if (units >= 4096) return 4096;
-  const int even = static_cast<int>((E / 2048 + 63) & ~int64_t(63));  // at most about 2,048 windows
-  return even < 64 ? 64 : even < 4096 ? even : 4096;
+  int64_t T = E / 2048;
+  if (units >= 1024) T = std::max(T, static_cast<int64_t>(E) / n_rows * 2);
+  return static_cast<int>(std::min<int64_t>(std::max<int64_t>((T + 63) & ~int64_t(63), 64), 4096));
 }
 
 egnn_status make_shape_of(const egnn_attn_desc *d, const egnn_graph *g, Shape *s) {
@@ -1335,7 +1353,11 @@ int dot_parts(const Shape &s, int bytes) {
   const int64_t deg = s.E / (s.n_dst > 0 ? s.n_dst : 1);
   const int64_t v = static_cast<int64_t>(s.n_src) * s.K * s.C * bytes;
   const int64_t parts = 8 * ((v + 8 * kPartBytes - 1) / (8 * kPartBytes));
-  return parts * 8 <= deg ? static_cast<int>(parts) : deg >= 32 && s.n_dst < 1024 ? 8 : 1;
+  if (parts * 8 > deg) return deg >= 32 && s.n_dst < 1024 ? 8 : 1;
+  // few rows: more parts, down to 8 edges each, until waves fill the chip
+  int64_t n = parts;
+  while (n * s.n_dst < 8192 && (n + 8) * 8 <= deg && n < 64) n += 8;
+  return static_cast<int>(n);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }

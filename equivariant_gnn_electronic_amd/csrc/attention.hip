@@ -231,6 +231,7 @@ __device__ inline float column_reduce(float v, int Hp, float (*red)[kWave], F f)
   for (int i = 1; i < kWaves; ++i) r = f(r, red[i][lane]);
   return r;
 }
+
 // exp(x), x <= 0 (or NaN): 2^t with t = x log2 e, whose rounding error r is
 // put back as a factor 1 + r ln 2.  Within 2 ulp for any x, where 2^t alone is
 // off by |x| / 2 ulp; infinity and what underflows give 0.
@@ -398,9 +399,10 @@ __device__ inline void team_sum(float (&dot)[U], const Team &tm) {
 
 // put(i, h, dot, first) for the edges i < cnt of i_first, i_first + stride, ...
 // (and, where a wave takes several at once, those that follow each), dot = sum
-// over the head's vectors of A . B[scol[i]] (row 0 for a source of -1).  A stays in registers, NIT vectors a lane; what does
-// not fit is added by further rounds (first = false).  ONE: a wave takes one
-// edge at a time, so the row's address is scalar work.
+// over the head's vectors of A . B[scol[i]] (row 0 for a source of -1).  A
+// stays in registers, NIT vectors a lane; what does not fit is added by further
+// rounds (first = false).  ONE: a wave takes one edge at a time, so the row's
+// address is scalar work.
 template <typename TA, typename TB, int VW, int NIT, bool ONE, typename Put>
 __device__ inline void edge_dots(const TA *arow, const TB *B, int64_t ldb, const int *scol, int i_first, int stride,
                                  int cnt, int K, int H, int C, const Team &tm, Put put) {
@@ -1199,39 +1201,56 @@ __global__ void __launch_bounds__(kThreads) gather_sum_kernel(const SumPair<TX, 
   Vec<TO, VW>::st(out + static_cast<int64_t>(row) * a.width + c, acc);
 }
 
-// Long rows: the pieces' sums added in a fixed order.  One block per window and
-// 64 columns, a wave a quarter of the pieces; it acts for the long row that
-// starts in its window, if any.
+// Sums whose pieces one launch joins, (group of rows, 64 columns) a block.
+template <typename TO> struct Joins {
+  SumArgs a[3];
+  TO *out[3];
+  int64_t begin[4] = {0, 0, 0, 0};  // first block of each; the end is begin[3]
+  int n = 0;
+};
+
+// Rows that a block of long_sum_kernel looks through: about 256 groups.
+__host__ __device__ inline int join_rows(int n_rows) { return n_rows < 512 ? 1 : n_rows < 16384 ? n_rows >> 8 : 64; }
+
+// Long rows: the pieces' sums added in a fixed order, a wave a quarter of the
+// pieces.  Mostly there are none, so what counts is finding that out: one
+// round of loads for a group of rows, and one launch for the backward's three
+// sums (3,000 rows: 5 us each by windows and apart, 15 by windows together, 6
+// us this way).
 template <typename TO>
-__global__ void __launch_bounds__(kThreads) long_sum_kernel(SumArgs a, TO *__restrict__ out) {
+__global__ void __launch_bounds__(kThreads) long_sum_kernel(const Joins<TO> js) {
   __shared__ float red[kWaves][kWave];
-  const int total = min(max(a.ptr[a.n_rows], 0), a.E);
-  const int64_t w0 = static_cast<int64_t>(blockIdx.x) * a.T;
-  if (w0 >= total) return;
-  const int row = owner(a, static_cast<int>(min(w0 + a.T, static_cast<int64_t>(total)) - 1));
-  if (row < 0 || row >= a.n_rows) return;
-  int b, e;
-  row_bounds(a.ptr, row, a.E, &b, &e);
-  if (e - b <= a.T || b < w0) return;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
-  const int c = blockIdx.y * kWave + lane, cc = min(c, a.width - 1);
-  const int n = piece_count(b, e, a.T);
-  const int upto = static_cast<int>(static_cast<int64_t>(n) * (wave + 1) / kWaves);
-  float s = 0.0f;
-  for (int i0 = static_cast<int>(static_cast<int64_t>(n) * wave / kWaves); i0 < upto; i0 += 8) {
-    float v[8];
+  for (int64_t block = blockIdx.x; block < js.begin[3]; block += gridDim.x) {
+    const int which = block < js.begin[1] ? 0 : block < js.begin[2] ? 1 : 2;
+    const SumArgs &a = js.a[which];
+    const int columns = (a.width + kWave - 1) / kWave, group = static_cast<int>((block - js.begin[which]) / columns);
+    const int c = static_cast<int>((block - js.begin[which]) % columns) * kWave + lane, cc = min(c, a.width - 1);
+    const int R = join_rows(a.n_rows), row0 = group * R;
+    int b = 0, e = 0;
+    if (lane < R && row0 + lane < a.n_rows) row_bounds(a.ptr, row0 + lane, a.E, &b, &e);
+    for (uint64_t left = __ballot(e - b > a.T); left; left &= left - 1) {
+      const int i = __ffsll(static_cast<unsigned long long>(left)) - 1;
+      const int first = __shfl(b, i), n = piece_count(first, __shfl(e, i), a.T);
+      const int upto = static_cast<int>(static_cast<int64_t>(n) * (wave + 1) / kWaves);
+      float s = 0.0f;
+      for (int i0 = static_cast<int>(static_cast<int64_t>(n) * wave / kWaves); i0 < upto; i0 += 8) {
+        float v[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      v[u] = a.part[static_cast<int64_t>(piece_id(b, a.T, min(i0 + u, n - 1))) * a.width + cc];
+        for (int u = 0; u < 8; ++u)
+          v[u] = a.part[static_cast<int64_t>(piece_id(first, a.T, min(i0 + u, n - 1))) * a.width + cc];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) s += i0 + u < upto ? v[u] : 0.0f;
+        for (int u = 0; u < 8; ++u) s += i0 + u < upto ? v[u] : 0.0f;
+      }
+      __syncthreads();  // the last row's sums are no longer read
+      red[wave][lane] = s;
+      __syncthreads();
+      if (wave != 0 || c >= a.width) continue;
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) s += red[w][lane];
+      Store<TO>::st(js.out[which] + static_cast<int64_t>(row0 + i) * a.width + c, s * a.scale);
+    }
   }
-  red[wave][lane] = s;
-  __syncthreads();
-  if (wave != 0 || c >= a.width) return;
-#pragma unroll
-  for (int i = 1; i < kWaves; ++i) s += red[i][lane];
-  Store<TO>::st(out + static_cast<int64_t>(row) * a.width + c, s * a.scale);
 }
 
 // ---------------------------------------------------------------------- host
@@ -1412,9 +1431,9 @@ size_t ws_fwd_of(const Shape &s, bool train) {
 
 size_t ws_bwd_of(const Shape &s) {
   const size_t E = s.E, H = s.H, P = plane(s);
-  const size_t part = std::max(sum_part_bytes(s.n_dst, s.n_src, s.E, 2 * s.H * s.D) +
-                                   sum_part_bytes(s.n_src, s.n_dst, s.E, 2 * s.H * s.D),
-                               sum_part_bytes(s.n_src, s.n_dst, s.E, s.K * s.C));
+  const size_t part = sum_part_bytes(s.n_dst, s.n_src, s.E, 2 * s.H * s.D) +
+                      sum_part_bytes(s.n_src, s.n_dst, s.E, 2 * s.H * s.D) +
+                      sum_part_bytes(s.n_src, s.n_dst, s.E, s.K * s.C);
   return align256(E * 2 * H * 4) + 2 * align256(E * H * 4) + 2 * align256(P * 2 * H * 4) + align256(P * H * 4) +
          align256(E * 4) + align256(static_cast<size_t>(s.n_dst) * H * 4) +
          align256(static_cast<size_t>(s.pieces) * H * 8) + part;
@@ -1492,20 +1511,28 @@ template <typename TX, typename TO> double sum_bytes(const SumArgs &a) {
          static_cast<double>(a.n_rows) * a.width * sizeof(TO);
 }
 
-template <typename TX, typename TO>
-egnn_status join_pieces(const SumKind &k, const SumArgs &a, TO *out, hipStream_t st) {
-  if (!k.pieces) return EGNN_OK;
+// A planned sum's pieces are joined once the others of js are launched, too.
+template <typename TO> void add_join(Joins<TO> &js, const SumKind &k, const SumArgs &a, TO *out) {
+  if (!k.pieces) return;
+  js.a[js.n] = a;
+  js.out[js.n] = out;
+  const int64_t end = js.begin[js.n] + static_cast<int64_t>(ceil_div(a.n_rows, join_rows(a.n_rows))) * ceil_div(a.width, kWave);
+  for (int i = ++js.n; i < 4; ++i) js.begin[i] = end;
+}
+
+template <typename TO> egnn_status join_pieces(const Joins<TO> &js, hipStream_t st) {
+  if (!js.n) return EGNN_OK;
   Timed t(st, "attn_long_sum", 0.0, 0.0);
-  long_sum_kernel<TO><<<dim3(static_cast<unsigned>(k.pieces / 2), ceil_div(a.width, kWave)), kThreads, 0, st>>>(
-      a, out);
+  long_sum_kernel<TO><<<static_cast<unsigned>(std::min<int64_t>(js.begin[3], kMaxBlocks)), kThreads, 0, st>>>(js);
   EGNN_CHECK_LAUNCH();
   return EGNN_OK;
 }
 
 template <typename TX, typename TO>
-egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream_t st) {
+egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, Joins<TO> &js, hipStream_t st) {
   if (a.n_rows == 0) return EGNN_OK;
   const SumKind k = plan_sum(a, X, out);
+  add_join(js, k, a, out);
   const int most = kMaxBlocks / a.S;  // blocks a slice in one launch
   for (; a.unit0 < a.units; a.unit0 += most * kWaves) {
     Timed t(st, name, a.unit0 ? 0.0 : 2.0 * a.E * a.width, a.unit0 ? 0.0 : sum_bytes<TX, TO>(a));
@@ -1514,14 +1541,14 @@ egnn_status run_sum(SumArgs a, const TX *X, TO *out, const char *name, hipStream
     const egnn_status r = launch_kind<TX, TO>(k, grid, SumPair<TX, TO>{{a, a}, {X, X}, {out, out}, grid}, st);
     if (r != EGNN_OK) return r;
   }
-  return join_pieces<TX, TO>(k, a, out, st);
+  return EGNN_OK;
 }
 
-// Two sums that need one kind of kernel share a launch; their pieces are
-// joined apart (each has its own part of the workspace).
+// Two sums that need one kind of kernel share a launch (each has its own part
+// of the workspace for its pieces).
 template <typename TX, typename TO>
 egnn_status run_two_sums(SumArgs a, const TX *Xa, TO *outa, const char *na, SumArgs b, const TX *Xb, TO *outb,
-                         const char *nb, const char *both, hipStream_t st) {
+                         const char *nb, const char *both, Joins<TO> &js, hipStream_t st) {
   SumArgs a2 = a, b2 = b;
   if (a.n_rows > 0 && b.n_rows > 0) {
     const SumKind ka = plan_sum(a2, Xa, outa), kb = plan_sum(b2, Xb, outb);
@@ -1532,19 +1559,15 @@ egnn_status run_two_sums(SumArgs a, const TX *Xa, TO *outa, const char *na, SumA
     const int64_t bytes = (static_cast<int64_t>(a.n_x) * a.width + static_cast<int64_t>(b.n_x) * b.width) *
                           static_cast<int64_t>(sizeof(TX));
     if (ka == kb && ga + gb <= kMaxBlocks && bytes <= kPairBytes) {
-      {
-        Timed t(st, both, 2.0 * a.E * (a.width + b.width), sum_bytes<TX, TO>(a2) + sum_bytes<TX, TO>(b2));
-        const egnn_status r =
-            launch_kind<TX, TO>(ka, static_cast<unsigned>(ga + gb),
-                                SumPair<TX, TO>{{a2, b2}, {Xa, Xb}, {outa, outb}, static_cast<unsigned>(ga)}, st);
-        if (r != EGNN_OK) return r;
-      }
-      const egnn_status r = join_pieces<TX, TO>(ka, a2, outa, st);
-      return r != EGNN_OK ? r : join_pieces<TX, TO>(kb, b2, outb, st);
+      add_join(js, ka, a2, outa);
+      add_join(js, kb, b2, outb);
+      Timed t(st, both, 2.0 * a.E * (a.width + b.width), sum_bytes<TX, TO>(a2) + sum_bytes<TX, TO>(b2));
+      return launch_kind<TX, TO>(ka, static_cast<unsigned>(ga + gb),
+                                 SumPair<TX, TO>{{a2, b2}, {Xa, Xb}, {outa, outb}, static_cast<unsigned>(ga)}, st);
     }
   }
-  const egnn_status r = run_sum<TX, TO>(a, Xa, outa, na, st);
-  return r != EGNN_OK ? r : run_sum<TX, TO>(b, Xb, outb, nb, st);
+  const egnn_status r = run_sum<TX, TO>(a, Xa, outa, na, js, st);
+  return r != EGNN_OK ? r : run_sum<TX, TO>(b, Xb, outb, nb, js, st);
 }
 
 template <typename T, int VW, bool ONE, int NIT = kMaxNit>
@@ -1636,7 +1659,9 @@ egnn_status forward(const Shape &s, const egnn_graph *g, const T *q, const T *k,
   m.width = s.K * s.C;
   m.scale = 1.0f;
   m.part = reinterpret_cast<float *>(ws);
-  return run_sum<T, T>(m, v, out, "attn_out", st);
+  Joins<T> js;
+  const egnn_status r = run_sum<T, T>(m, v, out, "attn_out", js, st);
+  return r != EGNN_OK ? r : join_pieces(js, st);
 }
 
 template <typename T>
@@ -1765,9 +1790,12 @@ egnn_status backward(const Shape &s, const egnn_graph *g, const T *q, const T *k
   m.n_x = s.n_dst;
   m.ldx = s.ldq;
   m.w = dlp_src;
-  m.part = part + sum_part_bytes(s.n_dst, s.n_src, s.E, m.width) / 4;  // both run at once
-  const egnn_status r =
-      run_two_sums<T, float>(to_q, k, gq, "attn_grad_q", m, q, gk, "attn_grad_k", "attn_grad_qk", st);
+  part += sum_part_bytes(s.n_dst, s.n_src, s.E, m.width) / 4;
+  m.part = part;
+  part += sum_part_bytes(s.n_src, s.n_dst, s.E, m.width) / 4;
+  Joins<float> js;
+  egnn_status r =
+      run_two_sums<T, float>(to_q, k, gq, "attn_grad_q", m, q, gk, "attn_grad_k", "attn_grad_qk", js, st);
   if (r != EGNN_OK) return r;
   m.part = part;
   m.ldx = static_cast<int64_t>(s.K) * s.C;
@@ -1777,7 +1805,8 @@ egnn_status backward(const Shape &s, const egnn_graph *g, const T *q, const T *k
   m.Ch = Ch;
   m.width = s.K * s.C;
   m.scale = 1.0f;
-  return run_sum<float, float>(m, go, gv, "attn_grad_v", st);
+  r = run_sum<float, float>(m, go, gv, "attn_grad_v", js, st);
+  return r != EGNN_OK ? r : join_pieces(js, st);
 }
 
 }  // namespace

@@ -87,6 +87,8 @@ CASES = {
     "steps_in_a_row_bf16": Case((900,) + (15,) * 40, 60, 2, 32, 4, 8, "bf16", mask=True),
     # many rows: cut at 4,096 edges only, so blocks take steps and pieces are joined
     "many_rows_and_a_long_one": Case((3,) * 500 + (9000,) + (2, 0, 5) * 200, 300, 0, 8, 2, 4, p=0.1),
+    # long rows next to each other, several of them joined by one block
+    "neighbouring_long_rows": Case((3,) * 600 + (4200, 4100, 1, 4300) + (2,) * 700, 9, 1, 16, 4, 8, p=0.1),
     # few rows of many edges: pieces longer than the shortest, none left over at the end
     "few_rows_of_many_edges": Case((140_000, 1), 50, 0, 2, 1, 2),
     # long component-free rows: slices that meet a few heads each

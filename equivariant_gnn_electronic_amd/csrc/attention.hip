@@ -18,11 +18,12 @@
 // sliced by columns and a product's rows are cut by source, one slice or part
 // an XCD, so that each 4 MB L2 holds its own share of the gathered array: the
 // rows then come from L2 rather than over the fabric (HfO2-like cell, 544,000
-// edges of 6.4 KB: out 340 us unsliced loads with vector addressing, 165 us
-// now, 21 TB/s, about 70% of the L2s' line rate; dots 374 us in one part, 153
-// in eight).  In bf16 the conversion to fp32 (two instructions a pair) beside
-// the multiply-adds is the limit: vector units busy 93% in out of the
-// GeSbTe-like cell (1.11 M edges, 471 us).
+// edges of 6.4 KB: out 340 us unsliced with vector addressing, 168 us now, 21
+// TB/s, 92% of the line requests hits; dots 374 us in one part, 152 in eight).
+// In bf16 the conversion to fp32 (two instructions a pair) beside the
+// multiply-adds is the limit: vector units busy 92% in out of the GeSbTe-like
+// cell (1.11 M edges of 6.4 KB, 361 us); its fp32 gradient of v (rows of 12.8
+// KB, 702 us, 20 TB/s) is at the lines again.
 //
 // Rows are handled by one block (logits, softmax) or one wave per slice or
 // part (sums, dots).  A row longer than the launch's limit T is cut at the
@@ -1209,13 +1210,13 @@ template <typename TO> struct Joins {
   int n = 0;
 };
 
-// Rows that a block of long_sum_kernel looks through: about 256 groups.
-__host__ __device__ inline int join_rows(int n_rows) { return n_rows < 512 ? 1 : n_rows < 16384 ? n_rows >> 8 : 64; }
+// Rows that a block of long_sum_kernel looks through: about 128 groups.
+__host__ __device__ inline int join_rows(int n_rows) { return n_rows < 256 ? 1 : n_rows < 8192 ? n_rows >> 7 : 64; }
 
 // Long rows: the pieces' sums added in a fixed order, a wave a quarter of the
 // pieces.  Mostly there are none, so what counts is finding that out: one
 // round of loads for a group of rows, and one launch for the backward's three
-// sums (3,000 rows: 5 us each by windows and apart, 15 by windows together, 6
+// sums (3,000 rows: 5 us each by windows and apart, 15 by windows together, 5
 // us this way).
 template <typename TO>
 __global__ void __launch_bounds__(kThreads) long_sum_kernel(const Joins<TO> js) {

@@ -36,7 +36,8 @@ __device__ inline int bucket_of(const float *borders, int n, float r) {
 }
 
 // A wave takes 64 edges: each lane finds one edge's bucket, then the lanes
-// write the 64 rows as one contiguous run, VW columns a lane.
+// write the 64 rows as one contiguous run, VW columns a lane.  (544,000 edges,
+// 16 columns, 37 MB: 10.7 us, 3.5 TB/s; a launch alone takes 3.)
 template <int VW>
 __global__ void __launch_bounds__(kThreads) bias_fwd_kernel(const float *__restrict__ dist, int64_t E,
                                                             const float *__restrict__ borders, int B, int M,
@@ -78,7 +79,8 @@ __global__ void __launch_bounds__(kThreads) bias_fwd_kernel(const float *__restr
 // belongs to one lane, which adds in edge order, so the sums are deterministic.
 // Four edges are read, added and written together, so that the chain through
 // LDS is one for four.  (3.15 M edges, 16 columns, 64 buckets: LDS float
-// atomics 299 us, at 222 cycles an instruction; one edge at a time 97 us.)
+// atomics 299 us, at 222 cycles an instruction; one edge at a time 97; four 75,
+// 2.9 TB/s, what the chains and nine waves a CU of 60 KB tables allow.)
 // Copies are summed in a fixed order at the end.
 // blockIdx.y picks a tile of Mt columns when a whole table does not fit.
 template <int U>

@@ -9,7 +9,9 @@
 // Bound: HBM traffic, one read of each input and one write.  A thread owns one
 // group of eight channels (one 16-byte load in bf16, two in fp32), which is
 // one generator call, and walks KC consecutive components with it, so the
-// rounds' integer products are spread over KC vectors.
+// rounds' integer products are spread over KC vectors.  Edge embeddings
+// (544,000 rows of 25 x 64, bf16, with residual): 960 us, 5.4 TB/s, vector
+// units busy 40%; node irreps (8,064 rows of 25 x 128, likewise): 27 us.
 #include <cmath>
 
 #include "common.h"

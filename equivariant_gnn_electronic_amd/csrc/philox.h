@@ -6,7 +6,7 @@
 // i, so one call decides eight consecutive i: 16-bit draw i%8, the low half of
 // each word first.  Decision i keeps iff its draw >= t, t = round(65536 p).
 // Sixteen bits a draw because the ten rounds' integer products, not memory,
-// would bound a mask that is spent on one element (measured at the kernels);
+// would bound a mask that is spent on one element;
 // they quantise p to 1/65536, and the factor 65536/(65536 - t) is that of the
 // quantised p, so the expectation is exact.
 #pragma once

@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(kThreads) bias_fwd_kernel(const float *__restr
 // belongs to one lane, which adds in edge order, so the sums are deterministic.
 // Four edges are read, added and written together, so that the chain through
 // LDS is one for four.  (3.15 M edges, 16 columns, 64 buckets: LDS float
-// atomics 299 us, at 222 cycles an instruction; one edge at a time 97; four 75,
-// 2.9 TB/s, what the chains and nine waves a CU of 60 KB tables allow.)
+// atomics 299 us, at 222 cycles an instruction; one edge at a time 97; four 62,
+// 3.5 TB/s, what the chains and nine waves a CU of 48 KB tables allow.)
 // Copies are summed in a fixed order at the end.
 // blockIdx.y picks a tile of Mt columns when a whole table does not fit.
 template <int U>
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads) bias_bwd_kernel(const float *__restr
   for (int i = threadIdx.x; i < B - 1; i += blockDim.x) sb[i] = borders[i];
   for (int i = threadIdx.x; i < copies * B * Mt; i += blockDim.x) tab[i] = 0.0f;
   __syncthreads();
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c0 = blockIdx.y * Mt;
   const int mt = M - c0 < Mt ? M - c0 : Mt;
   const int grp = lane / Mt, c = lane - grp * Mt;
@@ -103,9 +103,17 @@ __global__ void __launch_bounds__(kThreads) bias_bwd_kernel(const float *__restr
   float *mine = tab + ((wave * groups + (grp < groups ? grp : 0)) * B) * Mt + (c < Mt ? c : 0);
   const int ge = grp < groups ? grp : 0;
   const int64_t step = static_cast<int64_t>(gridDim.x) * waves * kWave;
+  const uint32_t own = static_cast<uint32_t>(ge * M + (c < mt ? c : 0));
   // a round is U edges of every group; the next round's loads are under way
-  // while one is added (addresses past the end are clamped, their values not used)
+  // while one is added (addresses past the end are clamped, their values not
+  // used; before it the wave's part of an address is scalar work: 75 us to 67)
   const auto load = [&](int64_t base, int i0, float (&v)[U]) {
+    if (base + i0 + groups * U <= E) {
+      const float *g = grad + (base + i0) * M + c0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = (g + u * groups * M)[own];
+      return;
+    }
     const int64_t left = E - base - 1;
     const float *g = grad + base * M + c0 + (c < mt ? c : 0);
 #pragma unroll
@@ -130,16 +138,17 @@ __global__ void __launch_bounds__(kThreads) bias_bwd_kernel(const float *__restr
         for (int u = 0; u < U; ++u) cur[u] = v[u];
         const bool more = i0 + groups * U < cnt;
         if (more || after < E) load(more ? base : after, more ? i0 + groups * U : 0, v);
+        if (i0 + groups * U > cnt) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) cur[u] = i0 + u * groups + ge < cnt ? cur[u] : 0.0f;
+        }
 #pragma unroll
         for (int u = 0; u < U; u += 4) {
           int at[4];
-          float x[4], t[4];
+          float t[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int e = i0 + (u + k) * groups + ge;
-            at[k] = __shfl(bk, e & (kWave - 1));
-            x[k] = e < cnt ? cur[u + k] : 0.0f;
-          }
+          for (int k = 0; k < 4; ++k)  // of edge i0 + (u + k) groups + ge, counted modulo 64
+            at[k] = __builtin_amdgcn_ds_bpermute((i0 + (u + k) * groups) * 4 + ge * 4, bk);
           if (on) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) t[k] = mine[at[k]];
@@ -148,7 +157,7 @@ __global__ void __launch_bounds__(kThreads) bias_bwd_kernel(const float *__restr
             for (int k = 0; k < 4; ++k) {
 #pragma unroll
               for (int j = 0; j < k; ++j) t[k] = at[j] == at[k] ? t[j] : t[k];
-              t[k] += x[k];
+              t[k] += cur[u + k];
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) mine[at[k]] = t[k];

@@ -20,8 +20,9 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kMaxBuckets = 1024;
 constexpr int kMaxColumns = 64;
 constexpr int kTableLds = 8192;       // floats of a table that is staged in LDS (32 KB)
-constexpr int kGradLds = 15360;       // floats of private tables in a block (60 KB, beside the borders)
-constexpr int kMaxGradBlocks = 768;   // partial tables of a gradient: up to three blocks on each of the 256 CUs
+constexpr int kGradLds = 12544;       // floats of private tables in a block (49 KB: with the borders three blocks a CU)
+constexpr int kCUs = 256;
+constexpr int kLdsOfCU = 160 * 1024;
 
 // number of borders <= r in an ascending list (NaN: 0); the answer lies in
 // 0..n whatever the list holds
@@ -88,6 +89,7 @@ __global__ void __launch_bounds__(kThreads) bias_bwd_kernel(const float *__restr
                                                             const float *__restrict__ borders, int B, int M, int Mt,
                                                             int groups, int copies,
                                                             const float *__restrict__ grad, float *__restrict__ part) {
+  constexpr int Q = U < 4 ? U : 4;       // edges read, added and written together
   extern __shared__ float lds[];
   float *sb = lds;                       // [B]
   float *tab = lds + ((B + 3) & ~3);     // [copies][B][Mt]
@@ -143,24 +145,24 @@ __global__ void __launch_bounds__(kThreads) bias_bwd_kernel(const float *__restr
           for (int u = 0; u < U; ++u) cur[u] = i0 + u * groups + ge < cnt ? cur[u] : 0.0f;
         }
 #pragma unroll
-        for (int u = 0; u < U; u += 4) {
-          int at[4];
-          float t[4];
+        for (int u = 0; u < U; u += Q) {
+          int at[Q];
+          float t[Q];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)  // of edge i0 + (u + k) groups + ge, counted modulo 64
+          for (int k = 0; k < Q; ++k)  // of edge i0 + (u + k) groups + ge, counted modulo 64
             at[k] = __builtin_amdgcn_ds_bpermute((i0 + (u + k) * groups) * 4 + ge * 4, bk);
           if (on) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) t[k] = mine[at[k]];
-            // an edge of the same bucket as an earlier one of the four adds to that one's sum
+            for (int k = 0; k < Q; ++k) t[k] = mine[at[k]];
+            // an edge of the same bucket as an earlier one of the round's adds to that one's sum
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < Q; ++k) {
 #pragma unroll
               for (int j = 0; j < k; ++j) t[k] = at[j] == at[k] ? t[j] : t[k];
               t[k] += cur[u + k];
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mine[at[k]] = t[k];
+            for (int k = 0; k < Q; ++k) mine[at[k]] = t[k];
           }
         }
       }
@@ -204,6 +206,25 @@ struct GradPlan {
   int Mt, groups, waves, blocks;
 };
 
+// Edges of a group in one round.  A wave's 64 edges are covered by whole rounds
+// of groups * U places, of which those past the last edge are work for nothing,
+// and a round costs about as much as one more edge a group.  (3.15 M edges, 64
+// buckets, 16 for any number of columns against this: 1 column 68 and 31 us, 2
+// columns 65 and 33, 6 columns 81 and 62, 8 columns 64 and 44.)
+int edges_a_round(int groups) {
+  int best = 1;
+  int least = INT32_MAX;
+  for (const int U : {16, 8, 4, 2, 1}) {
+    const int rounds = (kWave + groups * U - 1) / (groups * U);
+    const int cost = rounds * (U + 1);
+    if (cost < least) {
+      least = cost;
+      best = U;
+    }
+  }
+  return best;
+}
+
 // Columns per tile, edge groups per wave and waves per block so that the
 // block's private tables fit LDS.
 GradPlan grad_plan(int B, int M, int64_t E) {
@@ -216,8 +237,12 @@ GradPlan grad_plan(int B, int M, int64_t E) {
   if (p.groups > fit) p.groups = fit;
   p.waves = fit / p.groups;
   if (p.waves > kWaves) p.waves = kWaves;
-  const int64_t want = (E + p.waves * kWave - 1) / (p.waves * kWave);
-  p.blocks = static_cast<int>(want < 1 ? 1 : want > kMaxGradBlocks ? kMaxGradBlocks : want);
+  // a partial table for each block that the CUs hold at once, so that all of them
+  // run together (6 columns, 64 buckets: 62 us where 768 blocks of 60 KB do not
+  // fit at once, 46; 16 columns, 500 buckets: 417 with three blocks a CU, 345)
+  const int at_once = kLdsOfCU / (4 * (B + 3 + p.waves * p.groups * B * Mt) + 1024);
+  const int64_t most = kCUs * (at_once > 8 ? 8 : at_once), want = (E + p.waves * kWave - 1) / (p.waves * kWave);
+  p.blocks = static_cast<int>(want < 1 ? 1 : want > most ? most : want);
   return p;
 }
 
@@ -307,8 +332,13 @@ extern "C" egnn_status egnn_distance_bias_bwd(const egnn_bias_desc *d, const egn
   {
     Timed t(stream, "distance_bias_bwd", static_cast<double>(E) * M, 4.0 * static_cast<double>(E) * (M + 1));
     const dim3 grid(p.blocks, (M + p.Mt - 1) / p.Mt);
-    bias_bwd_kernel<16><<<grid, p.waves * kWave, lds, stream>>>(g->dist, E, borders, B, M, p.Mt, p.groups, copies,
-                                                                grad_bias, part);
+    const int U = edges_a_round(p.groups);
+    const auto kernel = U == 16  ? bias_bwd_kernel<16>
+                        : U == 8 ? bias_bwd_kernel<8>
+                        : U == 4 ? bias_bwd_kernel<4>
+                        : U == 2 ? bias_bwd_kernel<2>
+                                 : bias_bwd_kernel<1>;
+    kernel<<<grid, p.waves * kWave, lds, stream>>>(g->dist, E, borders, B, M, p.Mt, p.groups, copies, grad_bias, part);
     EGNN_CHECK_LAUNCH();
   }
   Timed t(stream, "distance_bias_sum", static_cast<double>(p.blocks) * B * M, 4.0 * (p.blocks + 1.0) * B * M);

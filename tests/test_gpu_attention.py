@@ -517,6 +517,34 @@ def test_distance_bias(dev, E, B, M):
     assert torch.equal(gt, eg.egnn_distance_bias_bwd(graph, borders.to(dev), G.to(dev)))
 
 
+@pytest.mark.parametrize("E,B,M", [(1_000_003, 20, 1), (1_000_003, 20, 2), (600_007, 40, 5), (600_007, 64, 9),
+                                   (600_007, 48, 12), (400_013, 500, 16)])
+def test_distance_bias_gradient_over_many_chunks(dev, E, B, M):
+    """Every round size of the gradient, waves that take several chunks, the last of them ragged."""
+    print(f"[bias gradient] {E} {B} {M}", flush=True)
+    g = torch.Generator().manual_seed(M)
+    borders = eg.egnn_distance_borders(B, B // 2, 4.0, 8.0)
+    dist, G = torch.rand(E, generator=g) * 10, torch.randn(E, M, generator=g)
+    graph = eg.Graph.from_csr(torch.tensor([0, E], dtype=torch.int32, device=dev),
+                              torch.zeros(E, dtype=torch.int32, device=dev))
+    graph.dist = dist.to(dev)
+    gt = eg.egnn_distance_bias_bwd(graph, borders.to(dev), G.to(dev))
+    b = oa.buckets(dist.numpy(), borders.numpy())
+    n = np.bincount(b, minlength=B)[:, None]
+    sums = [np.stack([np.bincount(b, t[:, c].double().numpy(), B) for c in range(M)], 1) for t in (G, G.abs())]
+    # a sum of n terms in any order: (n - 1) roundings of partial sums, each at most the sum of magnitudes
+    within(gt.cpu().numpy(), sums[0], n * oa.U32 * sums[1], None, "grad_table")
+    assert torch.equal(gt, eg.egnn_distance_bias_bwd(graph, borders.to(dev), G.to(dev)))
+    # integers add without rounding: an edge lost or counted twice shows
+    ones = torch.ones(E, M, device=dev)
+    assert np.array_equal(eg.egnn_distance_bias_bwd(graph, borders.to(dev), ones).cpu().numpy(),
+                          np.broadcast_to(n.astype(np.float32), (B, M)))
+    # what is not a number stays in its bucket
+    ones[E // 2] = float("nan")
+    bad = torch.isnan(eg.egnn_distance_bias_bwd(graph, borders.to(dev), ones)).cpu().numpy()
+    assert bad[b[E // 2]].all() and bad.sum() == M
+
+
 def test_distance_bias_without_edges(dev):
     graph = eg.Graph.from_csr(torch.zeros(2, dtype=torch.int32, device=dev), torch.zeros(0, dtype=torch.int32, device=dev))
     graph.dist = torch.zeros(0, device=dev)

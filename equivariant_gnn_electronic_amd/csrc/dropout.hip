@@ -31,8 +31,9 @@ struct DropShape {
   int KP;           // parts of the component axis (K = KP * KC)
 };
 
-template <typename T> struct Eight;
-template <> struct Eight<float> {
+// VW neighbouring channels
+template <typename T, int VW> struct Span;
+template <> struct Span<float, 8> {
   __device__ static inline void ld(const float *p, float (&v)[8]) {
     const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
@@ -43,7 +44,7 @@ template <> struct Eight<float> {
     reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
   }
 };
-template <> struct Eight<uint16_t> {
+template <> struct Span<uint16_t, 8> {
   __device__ static inline void ld(const uint16_t *p, float (&v)[8]) {
     const uint4 a = *reinterpret_cast<const uint4 *>(p);
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -62,58 +63,88 @@ template <> struct Eight<uint16_t> {
   }
 };
 
+template <> struct Span<float, 2> {
+  __device__ static inline void ld(const float *p, float (&v)[2]) {
+    const float2 a = *reinterpret_cast<const float2 *>(p);
+    v[0] = a.x; v[1] = a.y;
+  }
+  __device__ static inline void st(float *p, const float (&v)[2]) {
+    *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+  }
+};
+template <> struct Span<uint16_t, 2> {
+  __device__ static inline void ld(const uint16_t *p, float (&v)[2]) {
+    const uint32_t a = *reinterpret_cast<const uint32_t *>(p);
+    v[0] = __uint_as_float(a << 16);
+    v[1] = __uint_as_float(a & 0xFFFF0000u);
+  }
+  __device__ static inline void st(uint16_t *p, const float (&v)[2]) {
+    *reinterpret_cast<uint32_t *>(p) =
+        static_cast<uint32_t>(f32_to_bf16(v[0])) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16);
+  }
+};
+template <typename T> struct Span<T, 1> {
+  __device__ static inline void ld(const T *p, float (&v)[1]) { v[0] = Store<T>::ld(p); }
+  __device__ static inline void st(T *p, const float (&v)[1]) { Store<T>::st(p, v[0]); }
+};
+
 __device__ inline int degree_of(int k) {  // floor(sqrt(k)) for k < 81
   int l = 0;
   while ((l + 1) * (l + 1) <= k) ++l;
   return l;
 }
 
-// Keep factors of the eight channels at c0 of (row, degree l).  C is a
-// multiple of 8 here, so the eight decisions are one generator call.
-__device__ inline void factors8(const DropShape &s, const Drop &d, const DropKey &key, int64_t row, int l, int c0,
-                                float (&m)[8]) {
+// Keep factors of the VW channels at c0 of (row, degree l).  C is a multiple
+// of VW, so the decisions lie in one generator call.
+template <int VW>
+__device__ inline void factors(const DropShape &s, const Drop &d, const DropKey &key, int64_t row, int l, int c0,
+                               float (&m)[VW]) {
   if (s.share == EGNN_DROP_ROW) {
     const float f = drop_one(row, d, key);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) m[u] = f;
+    for (int u = 0; u < VW; ++u) m[u] = f;
     return;
   }
   const int64_t base = s.share == EGNN_DROP_DEGREE ? (row * (s.L + 1) + l) * s.C + c0 : row * s.C + c0;
   const uint4 w = philox4x32(static_cast<uint64_t>(base) >> 3, key);
+  const int u0 = VW == 8 ? 0 : static_cast<int>(base & 7);
 #pragma unroll
-  for (int u = 0; u < 8; ++u) m[u] = drop_draw(w, u) >= d.t ? d.factor : 0.0f;
+  for (int u = 0; u < VW; ++u) m[u] = drop_draw(w, u0 + u) >= d.t ? d.factor : 0.0f;
 }
 
 // A dropped element is the residual (or 0) whatever x holds there, so that an
 // infinity or NaN in a dropped place does not come through.
 __device__ inline float apply(float m, float x, float r) { return m == 0.0f ? r : r + m * x; }
 
-// One thread: eight channels of KC consecutive components of one row.  Lanes
-// run over channel groups first, so a group of lanes streams consecutive lines.
-template <typename T, int KC, bool RES>
+// One thread: VW channels of KC consecutive components of one row, all of whose
+// loads are issued first.  Lanes run over channel groups first, so a group of
+// lanes streams consecutive lines.  VW is 8, or 2 or 1 where the channel count
+// or the alignment allows no more (50 channels, lmax 4, bf16, 600 MB: 131 us by
+// pairs, 5.115 TB/s would take 117; 234 element after element).
+template <typename T, int KC, bool RES, int VW>
 __global__ void __launch_bounds__(kThreads) dropout_vec_kernel(DropShape s, Drop d, int64_t row0, uint32_t n_threads,
                                                                const T *x, const T *res, T *y) {
   const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
   if (i >= n_threads) return;
-  const uint32_t CG = static_cast<uint32_t>(s.C) >> 3;
+  const uint32_t CG = static_cast<uint32_t>(s.C) / VW;
   const uint32_t g = i % CG, q = i / CG;
   const uint32_t kp = q % static_cast<uint32_t>(s.KP);
   const int64_t row = row0 + q / static_cast<uint32_t>(s.KP);
   const int k0 = static_cast<int>(kp) * KC;
-  const int64_t at = (row * s.K + k0) * s.C + static_cast<int64_t>(g) * 8;
-  float v[KC][8], r[KC][8];
+  const int64_t at = (row * s.K + k0) * s.C + static_cast<int64_t>(g) * VW;
+  float v[KC][VW], r[KC][VW];
 #pragma unroll
-  for (int j = 0; j < KC; ++j) Eight<T>::ld(x + at + static_cast<int64_t>(j) * s.C, v[j]);
+  for (int j = 0; j < KC; ++j) Span<T, VW>::ld(x + at + static_cast<int64_t>(j) * s.C, v[j]);
   if constexpr (RES) {
 #pragma unroll
-    for (int j = 0; j < KC; ++j) Eight<T>::ld(res + at + static_cast<int64_t>(j) * s.C, r[j]);
+    for (int j = 0; j < KC; ++j) Span<T, VW>::ld(res + at + static_cast<int64_t>(j) * s.C, r[j]);
   }
-  float m[8];
+  float m[VW];
   const bool every = d.t == 0;
   DropKey key{};
   if (every) {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) m[u] = 1.0f;
+    for (int u = 0; u < VW; ++u) m[u] = 1.0f;
   } else {
     key = drop_key(d);
   }
@@ -126,20 +157,25 @@ __global__ void __launch_bounds__(kThreads) dropout_vec_kernel(DropShape s, Drop
       ++l;
       fresh = fresh || s.share == EGNN_DROP_DEGREE;
     }
-    if (fresh && !every) factors8(s, d, key, row, l, static_cast<int>(g) * 8, m);
+    if (fresh && !every) factors<VW>(s, d, key, row, l, static_cast<int>(g) * VW, m);
     fresh = false;
-    float o[8];
+    float o[VW];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) o[u] = apply(m[u], v[j][u], RES ? r[j][u] : 0.0f);
-    Eight<T>::st(y + at + static_cast<int64_t>(j) * s.C, o);
+    for (int u = 0; u < VW; ++u) o[u] = apply(m[u], v[j][u], RES ? r[j][u] : 0.0f);
+    Span<T, VW>::st(y + at + static_cast<int64_t>(j) * s.C, o);
   }
 }
 
-// Invariants (one component) with a decision per element: the decisions run
-// over the flat array, so groups of eight need no channel count that fits.
+// Invariants (one component): eight elements of the flat array a thread,
+// whatever the channel count.  The decisions run over the same array (one
+// generator call), or over its rows (C elements each; one call, or two where
+// the eight rows of a call end).  (500,000 rows of 33, bf16, by row: 30 us, 90
+// with a thread and a call an element.  Rows of whole eights keep the kernel
+// above, whose addresses are simpler: 64 channels, fp32, 73 us against 79.)
 template <typename T, bool RES>
-__global__ void __launch_bounds__(kThreads) dropout_flat_kernel(Drop d, int64_t group0, uint32_t n_groups, int64_t n,
-                                                                const T *x, const T *res, T *y) {
+__global__ void __launch_bounds__(kThreads) dropout_flat_kernel(Drop d, bool by_row, uint32_t C, int64_t group0,
+                                                                uint32_t n_groups, int64_t n, const T *x, const T *res,
+                                                                T *y) {
   const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
   if (i >= n_groups) return;
   const int64_t j = group0 + i, at = j * 8;
@@ -147,6 +183,22 @@ __global__ void __launch_bounds__(kThreads) dropout_flat_kernel(Drop d, int64_t 
   if (d.t == 0) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) m[u] = 1.0f;
+  } else if (by_row) {
+    const DropKey key = drop_key(d);
+    uint64_t row = static_cast<uint64_t>(at) / C;
+    uint32_t c = static_cast<uint32_t>(static_cast<uint64_t>(at) - row * C);
+    uint4 w = philox4x32(row >> 3, key);
+    float f = drop_draw(w, static_cast<int>(row & 7)) >= d.t ? d.factor : 0.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      m[u] = f;
+      if (++c == C) {
+        c = 0;
+        ++row;
+        if ((row & 7) == 0) w = philox4x32(row >> 3, key);
+        f = drop_draw(w, static_cast<int>(row & 7)) >= d.t ? d.factor : 0.0f;
+      }
+    }
   } else {
     const uint4 w = philox4x32(static_cast<uint64_t>(j), drop_key(d));
 #pragma unroll
@@ -154,11 +206,11 @@ __global__ void __launch_bounds__(kThreads) dropout_flat_kernel(Drop d, int64_t 
   }
   if (at + 8 <= n) {
     float v[8], r[8], o[8];
-    Eight<T>::ld(x + at, v);
-    if constexpr (RES) Eight<T>::ld(res + at, r);
+    Span<T, 8>::ld(x + at, v);
+    if constexpr (RES) Span<T, 8>::ld(res + at, r);
 #pragma unroll
     for (int u = 0; u < 8; ++u) o[u] = apply(m[u], v[u], RES ? r[u] : 0.0f);
-    Eight<T>::st(y + at, o);
+    Span<T, 8>::st(y + at, o);
   } else {
 #pragma unroll
     for (int u = 0; u < 8; ++u)
@@ -167,50 +219,21 @@ __global__ void __launch_bounds__(kThreads) dropout_flat_kernel(Drop d, int64_t 
   }
 }
 
-// Any channel count and alignment: one thread per (row, part, channel), its
-// decision drawn alone and spread over its components.
-template <typename T, bool RES>
-__global__ void __launch_bounds__(kThreads) dropout_any_kernel(DropShape s, int KC, Drop d, int64_t row0,
-                                                               uint32_t n_threads, const T *x, const T *res, T *y) {
-  const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
-  if (i >= n_threads) return;
-  const uint32_t c = i % static_cast<uint32_t>(s.C), q = i / static_cast<uint32_t>(s.C);
-  const uint32_t kp = q % static_cast<uint32_t>(s.KP);
-  const int64_t row = row0 + q / static_cast<uint32_t>(s.KP);
-  float m = 1.0f;
-  DropKey key{};
-  if (d.t != 0) key = drop_key(d);
-  int l = -1;
-  const int k0 = static_cast<int>(kp) * KC;
-  for (int k = k0; k < k0 + KC; ++k) {
-    const int lk = degree_of(k);
-    if (d.t != 0 && (l < 0 || (lk != l && s.share == EGNN_DROP_DEGREE))) {
-      const int64_t idx = s.share == EGNN_DROP_ROW      ? row
-                          : s.share == EGNN_DROP_DEGREE ? (row * (s.L + 1) + lk) * s.C + c
-                                                        : row * s.C + c;
-      m = drop_one(idx, d, key);
-    }
-    l = lk;
-    const int64_t at = (row * s.K + k) * s.C + c;
-    Store<T>::st(y + at, apply(m, Store<T>::ld(x + at), RES ? Store<T>::ld(res + at) : 0.0f));
-  }
-}
-
-template <typename T, bool RES>
+template <typename T, bool RES, int VW>
 void launch_vec(int KC, unsigned grid, hipStream_t st, const DropShape &s, const Drop &d, int64_t row0, uint32_t n,
                 const T *x, const T *res, T *y) {
   switch (KC) {
-    case 1: dropout_vec_kernel<T, 1, RES><<<grid, kThreads, 0, st>>>(s, d, row0, n, x, res, y); break;
-    case 2: dropout_vec_kernel<T, 2, RES><<<grid, kThreads, 0, st>>>(s, d, row0, n, x, res, y); break;
-    case 3: dropout_vec_kernel<T, 3, RES><<<grid, kThreads, 0, st>>>(s, d, row0, n, x, res, y); break;
-    case 4: dropout_vec_kernel<T, 4, RES><<<grid, kThreads, 0, st>>>(s, d, row0, n, x, res, y); break;
-    case 5: dropout_vec_kernel<T, 5, RES><<<grid, kThreads, 0, st>>>(s, d, row0, n, x, res, y); break;
-    case 6: dropout_vec_kernel<T, 6, RES><<<grid, kThreads, 0, st>>>(s, d, row0, n, x, res, y); break;
-    default: dropout_vec_kernel<T, 7, RES><<<grid, kThreads, 0, st>>>(s, d, row0, n, x, res, y); break;
+    case 1: dropout_vec_kernel<T, 1, RES, VW><<<grid, kThreads, 0, st>>>(s, d, row0, n, x, res, y); break;
+    case 2: dropout_vec_kernel<T, 2, RES, VW><<<grid, kThreads, 0, st>>>(s, d, row0, n, x, res, y); break;
+    case 3: dropout_vec_kernel<T, 3, RES, VW><<<grid, kThreads, 0, st>>>(s, d, row0, n, x, res, y); break;
+    case 4: dropout_vec_kernel<T, 4, RES, VW><<<grid, kThreads, 0, st>>>(s, d, row0, n, x, res, y); break;
+    case 5: dropout_vec_kernel<T, 5, RES, VW><<<grid, kThreads, 0, st>>>(s, d, row0, n, x, res, y); break;
+    case 6: dropout_vec_kernel<T, 6, RES, VW><<<grid, kThreads, 0, st>>>(s, d, row0, n, x, res, y); break;
+    default: dropout_vec_kernel<T, 7, RES, VW><<<grid, kThreads, 0, st>>>(s, d, row0, n, x, res, y); break;
   }
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool aligned(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 template <typename T, bool RES>
 egnn_status run(const egnn_dropout_desc *e, int64_t n_rows, const Drop &d, const T *x, const T *res, T *y,
@@ -223,28 +246,30 @@ egnn_status run(const egnn_dropout_desc *e, int64_t n_rows, const Drop &d, const
   // components per thread: K = (lmax+1)^2 divides by lmax + 1; 4 and 3 for the two largest keep registers low
   const int KC = e->lmax <= 6 ? e->lmax + 1 : e->lmax == 7 ? 4 : 3;
   s.KP = s.K / KC;
-  const bool al = aligned16(x) && aligned16(y) && (!RES || aligned16(res));
+  const auto all_aligned = [&](size_t bytes) {
+    return aligned(x, bytes) && aligned(y, bytes) && (!RES || aligned(res, bytes));
+  };
   const int64_t n = n_rows * s.K * s.C;
   Timed t(st, name, static_cast<double>(n) * (RES ? 2 : 1), static_cast<double>(n) * sizeof(T) * (RES ? 3 : 2));
-  if (al && s.K == 1 && s.share != EGNN_DROP_ROW) {
+  const bool by_row = s.share == EGNN_DROP_ROW;
+  if (s.K == 1 && all_aligned(16) && !(by_row && s.C % 8 == 0)) {
     const int64_t groups = (n + 7) / 8;
     for (int64_t g0 = 0; g0 < groups; g0 += kMaxThreads) {
       const uint32_t m = static_cast<uint32_t>(groups - g0 < kMaxThreads ? groups - g0 : kMaxThreads);
-      dropout_flat_kernel<T, RES><<<ceil_div(m, kThreads), kThreads, 0, st>>>(d, g0, m, n, x, res, y);
+      dropout_flat_kernel<T, RES><<<ceil_div(m, kThreads), kThreads, 0, st>>>(d, by_row, s.C, g0, m, n, x, res, y);
       EGNN_CHECK_LAUNCH();
     }
     return EGNN_OK;
   }
-  const bool vec = al && s.C % 8 == 0;
-  const int64_t per_row = static_cast<int64_t>(vec ? s.C / 8 : s.C) * s.KP;
+  const int VW = s.C % 8 == 0 && all_aligned(16) ? 8 : s.C % 2 == 0 && all_aligned(2 * sizeof(T)) ? 2 : 1;
+  const int64_t per_row = static_cast<int64_t>(s.C / VW) * s.KP;
   const int64_t rows_max = kMaxThreads / per_row;
   for (int64_t r0 = 0; r0 < n_rows; r0 += rows_max) {
     const int64_t rows = n_rows - r0 < rows_max ? n_rows - r0 : rows_max;
     const uint32_t m = static_cast<uint32_t>(rows * per_row);
-    if (vec)
-      launch_vec<T, RES>(KC, ceil_div(m, kThreads), st, s, d, r0, m, x, res, y);
-    else
-      dropout_any_kernel<T, RES><<<ceil_div(m, kThreads), kThreads, 0, st>>>(s, KC, d, r0, m, x, res, y);
+    if (VW == 8) launch_vec<T, RES, 8>(KC, ceil_div(m, kThreads), st, s, d, r0, m, x, res, y);
+    else if (VW == 2) launch_vec<T, RES, 2>(KC, ceil_div(m, kThreads), st, s, d, r0, m, x, res, y);
+    else launch_vec<T, RES, 1>(KC, ceil_div(m, kThreads), st, s, d, r0, m, x, res, y);
     EGNN_CHECK_LAUNCH();
   }
   return EGNN_OK;

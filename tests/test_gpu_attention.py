@@ -557,7 +557,8 @@ def test_distance_bias_without_edges(dev):
 
 @pytest.mark.parametrize("share", ["channel", "degree", "row"])
 @pytest.mark.parametrize("rows,lmax,C", [(1, 0, 1), (5, 0, 190), (70, 0, 64), (9, 1, 7), (33, 2, 8), (21, 3, 50),
-                                         (13, 4, 128), (4, 5, 16), (6, 6, 64), (3, 7, 24), (2, 8, 40)])
+                                         (13, 4, 128), (4, 5, 16), (6, 6, 64), (3, 7, 24), (2, 8, 40),
+                                         (100, 0, 3), (50, 0, 1), (41, 0, 13), (9, 5, 10), (3, 7, 9), (2, 8, 41)])
 def test_dropout(dev, rows, lmax, C, share):
     print(f"[dropout] {rows} {lmax} {C} {share}", flush=True)
     gen = torch.Generator().manual_seed(rows + C)

@@ -508,15 +508,49 @@ struct LogitArgs {
   float2 *piece_stats;            // [pieces][2H]
 };
 
-// Edge weights of [b, b + cnt) whose logits are in a.maps.
-__device__ inline void edge_weights(const LogitArgs &a, const float2 *fin, int b, int cnt) {
-  float2 *maps = a.maps + static_cast<int64_t>(b) * a.H;
-  for_decisions(b, cnt, a.H, a.drop, [&](int at, int i, int h, float m) {
-    const float2 l = maps[at];
-    const float2 al = make_float2(weight_of(l.x, fin[2 * h]), weight_of(l.y, fin[2 * h + 1]));
-    if (a.keep) maps[at] = al;
-    a.w[h * a.ldw + b + i] = m == 0.0f ? 0.0f : m * (al.x - a.lam[h] * al.y);
-  });
+// Writes the weights m x(i, h) of edges [b, b + cnt) to their planes.  A thread
+// writes its edge's heads, so that a wave's lanes write neighbouring edges of a
+// plane, and draws eight decisions at a time.
+template <typename X> __device__ inline void put_weights(const LogitArgs &a, int b, int cnt, X x) {
+  DropKey key{};
+  if (a.drop.t != 0) key = drop_key(a.drop);
+  for (int i = threadIdx.x; i < cnt; i += kThreads) {
+    const int64_t at = static_cast<int64_t>(b + i) * a.H;
+    // heads of one draw group after another; the groups start at multiples of 8 of at + h
+    for (int h0 = -static_cast<int>(at & 7); h0 < a.H; h0 += 8) {
+      uint4 draws = make_uint4(0, 0, 0, 0);
+      if (a.drop.t != 0) draws = philox4x32(static_cast<uint64_t>((at + h0) >> 3), key);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int h = h0 + u;
+        if (h < 0 || h >= a.H) continue;
+        float w = x(i, h);
+        if (a.drop.t != 0) w = drop_draw(draws, u) >= a.drop.t ? w * a.drop.factor : 0.0f;
+        a.w[h * a.ldw + b + i] = w;
+      }
+    }
+  }
+}
+
+// Edge weights of [b, e) whose logits are in a.maps, T edges at a time through
+// lds [T][H + 1].  (Pieces of 373,000 edges, 16 heads, training: 75 us with a
+// thread's eight weights straight to their planes, 43 so.)
+__device__ inline void edge_weights(const LogitArgs &a, const float2 *fin, int b, int e, float *lds) {
+  const int H = a.H, pitch = H + 1;
+  for (int c0 = b; c0 < e; c0 += a.T) {
+    const int cnt = min(a.T, e - c0);
+    float2 *maps = a.maps + static_cast<int64_t>(c0) * H;
+    __syncthreads();  // the last chunk's are no longer read
+    for (int f = threadIdx.x; f < cnt * H; f += kThreads) {
+      const int i = f / H, h = f - i * H;
+      const float2 l = maps[f];
+      const float2 al = make_float2(weight_of(l.x, fin[2 * h]), weight_of(l.y, fin[2 * h + 1]));
+      if (a.keep) maps[f] = al;
+      lds[i * pitch + h] = al.x - a.lam[h] * al.y;
+    }
+    __syncthreads();
+    put_weights(a, c0, cnt, [&](int i, int h) { return lds[i * pitch + h]; });
+  }
 }
 
 // One block per row (or piece): logits, T edges at a time, with the running
@@ -600,7 +634,7 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *
   if (!whole) {
     if (r0 == 0 && col < H2) fin[col] = st;
     __syncthreads();  // orders the logits that this block wrote to memory, too
-    edge_weights(a, fin, b, e - b);
+    edge_weights(a, fin, b, e, lg);
     return;
   }
   const int cnt = e - b;
@@ -611,30 +645,12 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(LogitArgs a, const T *
       if (a.keep) reinterpret_cast<float *>(a.maps)[static_cast<int64_t>(b + i) * H2 + col] = al;
     }
   __syncthreads();
-  // A thread writes its edge's heads, so that a wave's lanes write neighbouring
-  // edges of a plane, and draws eight decisions at a time.
-  DropKey key{};
-  if (a.drop.t != 0) key = drop_key(a.drop);
-  for (int i = threadIdx.x; i < cnt; i += kThreads) {
-    const int64_t at = static_cast<int64_t>(b + i) * a.H;
-    // heads of one draw group after another; the groups start at multiples of 8 of at + h
-    for (int h0 = -static_cast<int>(at & 7); h0 < a.H; h0 += 8) {
-      uint4 draws = make_uint4(0, 0, 0, 0);
-      if (a.drop.t != 0) draws = philox4x32(static_cast<uint64_t>((at + h0) >> 3), key);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int h = h0 + u;
-        if (h < 0 || h >= a.H) continue;
-        float w = lg[i * pitch + 2 * h] - slam[h] * lg[i * pitch + 2 * h + 1];
-        if (a.drop.t != 0) w = drop_draw(draws, u) >= a.drop.t ? w * a.drop.factor : 0.0f;
-        a.w[h * a.ldw + b + i] = w;
-      }
-    }
-  }
+  put_weights(a, b, cnt, [&](int i, int h) { return lg[i * pitch + 2 * h] - slam[h] * lg[i * pitch + 2 * h + 1]; });
 }
 
 // Long rows: the pieces' statistics joined, then their edge weights.
 __global__ void __launch_bounds__(kThreads) long_weights_kernel(LogitArgs a) {
+  extern __shared__ float lds[];  // [T][H + 1]
   __shared__ float red[kWaves][kWave];
   __shared__ float2 fin[kWave];
   const Piece pc = find_piece(blockIdx.x, a.TP, a.row_ptr, a.n_dst, a.E, [&](int pos) { return a.dst[pos]; });
@@ -663,7 +679,7 @@ __global__ void __launch_bounds__(kThreads) long_weights_kernel(LogitArgs a) {
   S = column_reduce(own == -INFINITY ? 0.0f : S * exp_of(own - M), Hp, red, SumOp());
   if (r0 == 0 && col < H2) fin[col] = finish_stats(M, S);
   __syncthreads();
-  edge_weights(a, fin, pc.begin, pc.end - pc.begin);
+  edge_weights(a, fin, pc.begin, pc.end, lds);
 }
 
 struct DotArgs {
@@ -1268,8 +1284,9 @@ struct Shape {
 
 // Edges beyond which a row is cut into pieces, for `units` waves over n_rows
 // rows.  Enough units fill the chip by themselves, and a piece costs one that
-// mostly finds nothing to do; with fewer, rows of up to twice the mean stay
-// whole; with few, rows are cut into about 2,048 pieces of 64 edges or more
+// mostly finds nothing to do; with fewer, rows of up to twice the mean and 512
+// stay whole (488 rows of 765 edges, 16 heads: logits and weights 159 us whole,
+// 141 cut); with few, rows are cut into about 2,048 pieces of 64 edges or more
 // (one row over 8,064 atoms: logits 20 us at 256, 9 at 64).  A small graph of
 // ordinary rows is not cut at all: that saves the launches that join pieces
 // (64 atoms, 2,900 edges, forward: 26 us in four launches, 18 in two).
@@ -1277,7 +1294,7 @@ int piece_edges(int64_t units, int n_rows, int E) {
   if (E <= 4096 && E <= static_cast<int64_t>(128) * n_rows) return E > 0 ? E : 1;
   if (units >= 4096) return 4096;
   int64_t T = E / 2048;
-  if (units >= 1024) T = std::max(T, static_cast<int64_t>(E) / n_rows * 2);
+  if (units >= 1024) T = std::max(T, std::min<int64_t>(static_cast<int64_t>(E) / n_rows * 2, 512));
   return static_cast<int>(std::min<int64_t>(std::max<int64_t>((T + 63) & ~int64_t(63), 64), 4096));
 }
 
@@ -1640,7 +1657,7 @@ egnn_status forward(const Shape &s, const egnn_graph *g, const T *q, const T *k,
     }
     if (s.pieces) {
       Timed t(st, "attn_long_weights", 0.0, 0.0);
-      long_weights_kernel<<<static_cast<unsigned>(s.pieces), kThreads, 0, st>>>(a);
+      long_weights_kernel<<<static_cast<unsigned>(s.pieces), kThreads, static_cast<size_t>(s.T) * (s.H + 1) * 4, st>>>(a);
       EGNN_CHECK_LAUNCH();
     }
   }

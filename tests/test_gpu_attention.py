@@ -89,6 +89,8 @@ CASES = {
     "many_rows_and_a_long_one": Case((3,) * 500 + (9000,) + (2, 0, 5) * 200, 300, 0, 8, 2, 4, p=0.1),
     # long rows next to each other, several of them joined by one block
     "neighbouring_long_rows": Case((3,) * 600 + (4200, 4100, 1, 4300) + (2,) * 700, 9, 1, 16, 4, 8, p=0.1),
+    # some hundred rows of several steps each, and a few that are cut at 512 edges
+    "some_hundred_rows": Case((300,) * 258 + (900, 513), 50, 0, 16, 16, 4, p=0.1),
     # few rows of many edges: pieces longer than the shortest, none left over at the end
     "few_rows_of_many_edges": Case((140_000, 1), 50, 0, 2, 1, 2),
     # long component-free rows: slices that meet a few heads each
